@@ -68,7 +68,7 @@ typedef void *gdn_stream_t;
 /* Status codes returned by every call. */
 #define GDN_OK 0
 #define GDN_ERR_NULL 1            /* a required pointer is NULL */
-#define GDN_ERR_DIMS 2            /* a size is out of the supported range, see gdn_dims */
+#define GDN_ERR_DIMS 2            /* a size is out of the supported range, see gdn_dims, attn_dims */
 #define GDN_ERR_ALIGN 3           /* a float state/checkpoint/output pointer is not 16-byte aligned */
 #define GDN_ERR_DTYPE 4           /* in_dtype is neither GDN_F32 nor GDN_BF16 */
 #define GDN_ERR_TREE_ROOT 5       /* parent[0] != -1 (malformed root) */
@@ -94,6 +94,12 @@ typedef void *gdn_stream_t;
                                      flag); its outputs are incomplete */
 #define GDN_DEV_BOUNDS 0x20       /* debug builds of the library only (GDN_DEBUG_BOUNDS): a kernel
                                      skipped a global access that fell outside its buffer */
+#define GDN_DEV_LENGTH 0x40       /* a context length, or a count of tokens asked for, that its row of
+                                     the page table (or the rotary table) cannot hold: the request
+                                     is left out */
+#define GDN_DEV_PAGE 0x80         /* a page id outside [0, n_pages) where a page is needed: read as
+                                     zeros, never written */
+#define GDN_DEV_POOL 0x100        /* no free page was left: what needed one is left out */
 
 /* Limits of this library. */
 #define GDN_MAX_TOKENS 64         /* n_tok (= N - 1) per span */
@@ -424,6 +430,217 @@ int spec_topk(int32_t rows, int32_t vocab, int32_t k, const float *logits,
 
 /* Bytes of workspace spec_topk needs; 0 if the sizes are out of range. */
 size_t spec_topk_workspace_bytes(int32_t rows, int32_t k);
+
+/*
+ * The full-attention layers of a hybrid target: their drafted span, their
+ * paged key/value cache, and the sampled form of the acceptance. These calls
+ * stand beside the GDN calls above in the same step (verify, accept, restore):
+ * attn_qk_norm_rope and attn_verify_span / attn_tree_verify per attention
+ * layer, spec_accept_sample in the place of spec_accept_greedy, kv_commit_path
+ * beside gdn_rollback_restore, and kv_pages_resize / kv_pages_fork between
+ * steps. The pages name the hybrid's attention layers and their KV cache
+ * (lucebox PR #506, Summary; openinfer PR #626, What Changed: committed KV)
+ * without printing equations; each call states its own.
+ *
+ * Cache of one layer: k_pages, v_pages [n_pages][h_kv][page_tokens][d_head],
+ * in_dtype. Token slot s of request b lies in page page_table[b][s /
+ * page_tokens] at row s % page_tokens. ctx_len[b] committed tokens lie in
+ * slots 0..ctx_len-1; the span's node t (t >= 1) has slot ctx_len + t - 1.
+ * Entries of page_table that no slot in use needs are not read. A request
+ * with ctx_len < 0 or ctx_len + n_tok > table_width * page_tokens is left
+ * out (GDN_DEV_LENGTH), a needed page id outside [0, n_pages) reads as zeros
+ * and is never written (GDN_DEV_PAGE).
+ *
+ *   batch        B >= 1 requests, B <= 65535
+ *   layers       Y >= 1 layers of the kv_* calls' caches [Y][n_pages]...;
+ *                the attn_* calls work on one layer and ignore it
+ *   h_q, h_kv    query and key/value heads, h_q % h_kv == 0, query head h
+ *                reads key/value head floor(h * h_kv / h_q); at most 1024
+ *   d_head       64, 128 or 256
+ *   page_tokens  16, 32, 64, 128 or 256
+ *   n_pages      pages of one layer's pool; n_pages * h_kv < 2^31
+ *   table_width  entries of a request's page table row;
+ *                table_width * page_tokens < 2^30, batch * table_width < 2^31
+ *   in_dtype     GDN_F32 or GDN_BF16: q, k, v, norm weights and out
+ */
+typedef struct attn_dims {
+    int32_t batch, layers, h_q, h_kv, d_head, page_tokens, n_pages, table_width;
+    int32_t in_dtype;
+} attn_dims;
+
+/*
+ * attn_qk_norm_rope — RMS norm of every query and key head, rotary embedding,
+ * and the span's keys and values into the cache, in one pass.
+ *
+ * For each new token t = 1..n_tok of each request, with x one head's d_head
+ * values of q or k and w that kind's norm weights,
+ *   y_i = x_i / sqrt(mean(x^2) + eps) * (w_i + norm_offset)
+ * then, on the first rot_dim values, with the position p = ctx_len +
+ * depth(t) - 1 and (c, s) = (cos, sin) of its row of the rotary table,
+ *   (y_i, y_j) <- (y_i c_m - y_j s_m,  y_j c_m + y_i s_m),   m < rot_dim / 2,
+ * for the pairs (i, j) = (m, m + rot_dim / 2), or (2m, 2m + 1) with
+ * GDN_ROPE_PAIRS. v is copied. Arithmetic in f32, rounded once at the store.
+ *
+ *   qkv         [B][n_tok] rows of qkv_stride elements (a multiple of 16 bytes),
+ *               each starting with q (h_q * d_head) | k (h_kv * d_head) | v (h_kv * d_head)
+ *   q_norm, k_norm [d_head] in_dtype; norm_offset 0, or 1 for weights stored
+ *               around zero; eps > 0
+ *   rope        [max_pos][rot_dim] f32: rot_dim / 2 cosines, then the sines.
+ *               May be NULL when rot_dim == 0 (no rotation)
+ *   rot_dim     0 or a multiple of 16, at most d_head
+ *   parent_dev  [B][n_tok + 1] for trees (n_tok <= GDN_MAX_TOKENS), NULL for
+ *               chains of any length (depth(t) = t). A parent outside [0, i)
+ *               is flagged GDN_DEV_TREE and taken as i - 1
+ *   q_out       [B][n_tok][h_q][d_head]
+ *   k_pages, v_pages  one layer's cache; slots ctx_len..ctx_len+n_tok-1 written
+ * A request with ctx_len + n_tok > max_pos is left out too (GDN_DEV_LENGTH;
+ * rot_dim 0: no such limit). Limits: n_tok >= 1, B * n_tok < 2^31. All
+ * pointers but the integer ones 16-byte aligned.
+ * Returns GDN_OK or GDN_ERR_{NULL,DIMS,ALIGN,DTYPE,FLAGS,CUDA}.
+ */
+#define GDN_ROPE_PAIRS 0x1u
+int attn_qk_norm_rope(const attn_dims *dims, int32_t n_tok, const void *qkv, int64_t qkv_stride,
+                      const void *q_norm, const void *k_norm, float eps, float norm_offset,
+                      const float *rope, int32_t rot_dim, int32_t max_pos,
+                      const int32_t *parent_dev, const int32_t *ctx_len, const int32_t *page_table,
+                      void *q_out, void *k_pages, void *v_pages, int32_t *dev_status,
+                      uint32_t flags, gdn_stream_t stream);
+
+/*
+ * attn_verify_span / attn_tree_verify — attention of a drafted chain or tree
+ * over the paged cache: for node t of 1..n_tok and each query head
+ *   o_t = sum_s softmax_s(scale q_t . k_s) v_s
+ * over the committed slots and the slots of the node's root path (chain: the
+ * nodes 1..t). One token (n_tok = 1) is plain decoding. Slots outside that set
+ * do not touch the result, whatever they hold; rows of a page past the last
+ * slot are not read as numbers.
+ *
+ *   q          [B][n_tok][h_q][d_head]
+ *   out        [B][n_tok][h_q][d_head], in_dtype; zeros for a request left out
+ *   workspace  at least attn_workspace_bytes(dims, n_tok) bytes, 256-byte
+ *              aligned, any contents; overlapping calls must not share it
+ *   parent_host, parent_dev as for gdn_tree_verify ([B][n_nodes], n_tok =
+ *              n_nodes - 1); a device parent outside [0, i) is flagged
+ *              GDN_DEV_TREE and taken as i - 1
+ * bf16: products on the tensor cores with f32 accumulation, softmax in f32, its
+ * weights rounded to bf16 for the second product; f32: all in f32.
+ * Limits: 1 <= n_tok <= GDN_MAX_TOKENS, batch * h_kv <= 65535, scale finite.
+ * Returns GDN_OK or GDN_ERR_{NULL,DIMS,ALIGN,DTYPE,TREE_*,WORKSPACE,CUDA}.
+ */
+int attn_verify_span(const attn_dims *dims, int32_t n_tok, const void *q, const void *k_pages,
+                     const void *v_pages, const int32_t *page_table, const int32_t *ctx_len,
+                     float scale, void *out, void *workspace, size_t workspace_bytes,
+                     int32_t *dev_status, gdn_stream_t stream);
+int attn_tree_verify(const attn_dims *dims, int32_t n_nodes, const int32_t *parent_host,
+                     const int32_t *parent_dev, const void *q, const void *k_pages,
+                     const void *v_pages, const int32_t *page_table, const int32_t *ctx_len,
+                     float scale, void *out, void *workspace, size_t workspace_bytes,
+                     int32_t *dev_status, gdn_stream_t stream);
+
+/* Bytes of workspace attn_verify_span (n_tok) or attn_tree_verify (n_tok =
+ * n_nodes - 1) needs; 0 if the sizes are out of range. */
+size_t attn_workspace_bytes(const attn_dims *dims, int32_t n_tok);
+
+/*
+ * spec_accept_sample — acceptance of drafted tokens by sampling, so that what
+ * is committed is distributed as the target's own samples. Random numbers are
+ * inputs. With p_n = softmax(logits row n / temperature) and the children of a
+ * node tried in index order, starting at the root:
+ *   draft_probs given (row n: the distribution q the children of n were drawn
+ *     from, independently): r = p_n; child i with token x is accepted if
+ *     uniforms[i] * q(x) < r(x), else r <- max(r - q, 0) normalised;
+ *   draft_probs NULL (fixed candidates): child i is accepted if uniforms[i] <
+ *     r(x), else r <- r without x, normalised;
+ *   accepted: continue at that child. No child left: the next token is the
+ *     largest r(v) / noise[v] (lowest index on ties), a sample of r when the
+ *     noise is exponential with mean 1. If r is zero everywhere, p_n is taken.
+ * Temperature 0 is the limit: p uniform over the largest logits. A NaN or +inf
+ * among a row's logits, or a row with none above -inf, makes its p NaN: its
+ * children are rejected, the next token after it is 0, and GDN_DEV_NAN_LOGIT
+ * is set. A token outside [0, vocab) is rejected (GDN_DEV_TOKEN_RANGE), a
+ * parent outside [0, i) leaves its node out (GDN_DEV_TREE).
+ *
+ *   logits      [B][N][V] f32, 4-byte aligned
+ *   draft_probs [B][N-1][V] f32 or NULL, 4-byte aligned
+ *   tokens      [B][N] int32, entry 0 ignored
+ *   parent_dev  [B][N] int32 for trees, NULL for chains
+ *   temperature [B] f32 (>= 0) or NULL (all 1)
+ *   uniforms    [B][N] f32 in [0, 1), entry 0 ignored
+ *   noise       [B][V] f32 > 0
+ * Outputs: accept_len [B], accept_node [B] as spec_accept_greedy;
+ *   next_token [B] int32; token_prob [B][N] f32 (nullable): entry n >= 1 the
+ *   target's p(tokens[n]) after its parent, entry 0 p(next_token) after the
+ *   accepted node.
+ *   workspace  at least spec_accept_sample_workspace_bytes(B, N) bytes,
+ *              256-byte aligned, any contents; overlapping calls must not share it
+ * Limits: 1 <= N <= GDN_MAX_TOKENS + 1, 1 <= V < 2^31, B <= 65535.
+ * Returns GDN_OK or GDN_ERR_{NULL,DIMS,ALIGN,WORKSPACE,CUDA}.
+ */
+int spec_accept_sample(int32_t batch, int32_t n_nodes, int32_t vocab, const float *logits,
+                       const float *draft_probs, const int32_t *tokens, const int32_t *parent_dev,
+                       const float *temperature, const float *uniforms, const float *noise,
+                       int32_t *accept_len, int32_t *accept_node, int32_t *next_token,
+                       float *token_prob, void *workspace, size_t workspace_bytes,
+                       int32_t *dev_status, gdn_stream_t stream);
+size_t spec_accept_sample_workspace_bytes(int32_t batch, int32_t n_nodes);
+
+/*
+ * kv_commit_path — after the acceptance, the accepted root path's keys and
+ * values moved together in every layer: the path's j-th node (j = 1..k, k =
+ * depth of accept_node) goes from slot ctx_len + node - 1 to ctx_len + j - 1,
+ * and ctx_out[b] = ctx_len[b] + k. What lies past the new length is left over.
+ *   parent_dev   [B][n_nodes] for trees; NULL for chains, whose path is in
+ *                place already (only ctx_out is written; the pools may be NULL)
+ *   accept_node  [B]; outside [0, n_nodes): the request keeps its length
+ *                (GDN_DEV_NODE_RANGE). A parent outside [0, i) is flagged
+ *                GDN_DEV_TREE and taken as i - 1
+ *   k_pages, v_pages [Y][n_pages][h_kv][page_tokens][d_head]
+ *   ctx_out      [B]; must not overlap ctx_len
+ * Limits: 2 <= n_nodes <= GDN_MAX_TOKENS + 1.
+ * Returns GDN_OK or GDN_ERR_{NULL,DIMS,ALIGN,DTYPE,CUDA}.
+ */
+int kv_commit_path(const attn_dims *dims, int32_t n_nodes, const int32_t *parent_dev,
+                   const int32_t *accept_node, const int32_t *ctx_len, const int32_t *page_table,
+                   void *k_pages, void *v_pages, int32_t *ctx_out, int32_t *dev_status,
+                   gdn_stream_t stream);
+
+/*
+ * Pages of the cache. page_ref[n_pages] int32 counts the table entries that
+ * name a page; a page is free while its count is 0, and the free page with the
+ * lowest id is taken first, so results do not depend on timing. A request's
+ * valid entries (>= 0) stand at the start of its row; the others are -1.
+ *
+ * kv_pages_resize — for every request b with want[b] >= 0 the row is made
+ * ceil(want[b] / page_tokens) entries long: first every request's entries
+ * beyond that are given back (count - 1, entry -1), then missing ones are
+ * taken, requests in order, each from its first missing entry on. want[b] < 0
+ * leaves the row as it is. A want[b] beyond the table is left out
+ * (GDN_DEV_LENGTH); an entry for which no page is free stays -1
+ * (GDN_DEV_POOL). want 0 frees a request; ctx_len trims a rejected span;
+ * ctx_len + n_tok makes room for the next.
+ *
+ * kv_pages_fork — request dst[i] becomes a copy of src[i], i = 0..n_fork-1 in
+ * order: pages full up to ctx_len[src] are shared (count + 1), a tail page's
+ * ctx_len % page_tokens live rows are copied in every layer into a page taken
+ * for it, the other entries become -1, and ctx_len[dst] = ctx_len[src]. What
+ * dst's row held before is overwritten, not given back: resize it to 0 first.
+ * The dst must differ from each other and from every src. An index outside
+ * [0, B), or a length that the table cannot hold, leaves out that fork
+ * (GDN_DEV_NODE_RANGE, GDN_DEV_LENGTH); one whose tail finds no free page
+ * makes dst empty: length 0, all entries -1 (GDN_DEV_POOL).
+ *
+ * workspace: at least kv_pages_workspace_bytes(dims) bytes, 256-byte aligned,
+ * any contents; overlapping calls must not share it.
+ * Return GDN_OK or GDN_ERR_{NULL,DIMS,ALIGN,DTYPE,WORKSPACE,CUDA}.
+ */
+int kv_pages_resize(const attn_dims *dims, const int32_t *want, int32_t *page_table,
+                    int32_t *page_ref, void *workspace, size_t workspace_bytes,
+                    int32_t *dev_status, gdn_stream_t stream);
+int kv_pages_fork(const attn_dims *dims, int32_t n_fork, const int32_t *src, const int32_t *dst,
+                  int32_t *page_table, int32_t *ctx_len, int32_t *page_ref,
+                  void *k_pages, void *v_pages, void *workspace, size_t workspace_bytes,
+                  int32_t *dev_status, gdn_stream_t stream);
+size_t kv_pages_workspace_bytes(const attn_dims *dims);
 
 /*
  * gdn_tree_check — host-only geometry check of B parent arrays of n_nodes

@@ -1,0 +1,15 @@
+// The attention kernels behind attn_verify_span and attn_tree_verify.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include "gdnspec.h"
+
+namespace gdnattn {
+
+struct AttnArgs;
+
+size_t simt_workspace(const attn_dims *d, int n_tok);
+int simt_launch(const attn_dims *d, const AttnArgs &a, void *workspace, cudaStream_t st);
+
+}  // namespace gdnattn

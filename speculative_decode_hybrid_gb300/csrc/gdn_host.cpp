@@ -47,6 +47,21 @@ int check_tree(const int32_t *parent, int32_t batch, int32_t n_nodes, bool requi
     return GDN_OK;
 }
 
+int check_attn(const attn_dims *d) {
+    if (!d) return GDN_ERR_NULL;
+    if (d->in_dtype != GDN_F32 && d->in_dtype != GDN_BF16) return GDN_ERR_DTYPE;
+    if (d->batch < 1 || d->batch > 65535 || d->layers < 1 || d->layers > 65535) return GDN_ERR_DIMS;
+    if (d->h_kv < 1 || d->h_q < d->h_kv || d->h_q > 1024 || d->h_q % d->h_kv != 0) return GDN_ERR_DIMS;
+    if (d->d_head != 64 && d->d_head != 128 && d->d_head != 256) return GDN_ERR_DIMS;
+    const int32_t p = d->page_tokens;
+    if (p != 16 && p != 32 && p != 64 && p != 128 && p != 256) return GDN_ERR_DIMS;
+    if (d->n_pages < 1 || (int64_t)d->n_pages * d->h_kv > 0x7fffffffLL) return GDN_ERR_DIMS;
+    if (d->table_width < 1 || (int64_t)d->table_width * p >= (1LL << 30) ||
+        (int64_t)d->batch * d->table_width > 0x7fffffffLL)
+        return GDN_ERR_DIMS;
+    return GDN_OK;
+}
+
 int sm_count() {
     static int cached[256] = {0};
     int dev = 0;

@@ -27,6 +27,15 @@ inline size_t conv_slot_elems(const gdn_dims *d) {
     return (size_t)d->conv_ch * (size_t)(d->conv_k - 1);
 }
 
+// Checks attn_dims (sizes and types; not the layer count of the attn_* calls).
+int check_attn(const attn_dims *d);
+
+// Elements of one layer's page pool.
+inline size_t pool_elems(const attn_dims *d) {
+    return (size_t)d->n_pages * (size_t)d->h_kv * (size_t)d->page_tokens * (size_t)d->d_head;
+}
+inline size_t attn_elem_bytes(const attn_dims *d) { return d->in_dtype == GDN_BF16 ? 2 : 4; }
+
 // SM count of the current device (cached per device); 0 on failure.
 int sm_count();
 

@@ -1,0 +1,474 @@
+// The paged key/value cache between steps: the accepted path's rows moved
+// together (kv_commit_path), pages given back and taken (kv_pages_resize),
+// requests forked (kv_pages_fork). (lucebox PR #506, Summary, and openinfer
+// PR #626, What Changed: the committed context's KV beside the recurrent
+// state.)
+//
+// All three are bound by latency at a few requests and by the bytes of the
+// moved rows at many. A page is free while its reference count is 0 and the
+// lowest free id is taken first, so that the counts are the only state of the
+// pool and integer atomics, in whatever order, give the same result.
+#include <cuda_runtime.h>
+
+#include <initializer_list>
+
+#include "gdn_device.cuh"
+#include "gdn_host.h"
+#include "gdnspec.h"
+
+namespace {
+
+using gdndev::Buf;
+
+constexpr int kMaxNodes = GDN_MAX_TOKENS + 1;
+
+// ---------------------------------------------------------------- commit
+
+struct CommitArgs {
+    int n_nodes, layers, h_kv, page_shift, n_pages, width, row_units;  // row_units: 16-byte units of one row
+    const int32_t *parent, *node, *ctx, *table;
+    uint4 *k, *v;
+    int32_t *ctx_out, *status;
+};
+
+constexpr int kCommitThreads = 256;
+constexpr int kCommitHold = 8;  // 16-byte units a thread holds between the reads and the writes
+
+// grid (parts, B). The slices of a request (pool, layer, head) are dealt out to
+// its CTAs. A path's destinations lie at or below its sources and may be other
+// nodes' sources, so a slice is read whole before it is written: a round takes
+// as many slices as the threads' registers hold (at least one: a path of 64
+// rows of 1 KB goes in column ranges).
+__global__ void __launch_bounds__(kCommitThreads) commit_path(CommitArgs a) {
+    __shared__ int32_t parent[kMaxNodes];
+    __shared__ int depth_of_last, in_place;
+    __shared__ long long src_row[GDN_MAX_TOKENS], dst_row[GDN_MAX_TOKENS];  // page * page_tokens * h_kv + offset; -1: no such page
+    const int b = blockIdx.y, tid = threadIdx.x, N = a.n_nodes;
+    const size_t B = gridDim.y;
+    int32_t *st = a.status;
+    const Buf bp{a.parent, B * N * 4}, bt{a.table, B * (size_t)a.width * 4};
+    const size_t slice_units = (size_t)a.row_units << a.page_shift;  // of one page and head
+    const size_t pool_bytes = (size_t)a.layers * a.n_pages * a.h_kv * slice_units * 16;
+    gdndev::pdl_wait();
+    const int node = a.node[b], ctx = a.ctx[b];
+    const bool fits = ctx >= 0 && (int64_t)ctx + N - 1 <= (int64_t)a.width << a.page_shift;
+    const bool known = node >= 0 && node < N;
+    if (!fits || !known) {
+        if (blockIdx.x == 0 && tid == 0) {
+            a.ctx_out[b] = ctx;
+            if (st) atomicOr(st, fits ? GDN_DEV_NODE_RANGE : GDN_DEV_LENGTH);
+        }
+        return;
+    }
+    if (a.parent) {
+        for (int i = tid; i < N; i += kCommitThreads) {
+            const int32_t *f = a.parent + (size_t)b * N + i;
+            int p = GDN_IN(f, 4, bp, st) ? *f : i - 1;
+            if (i > 0 && (p < 0 || p >= i)) {
+                p = i - 1;
+                if (blockIdx.x == 0 && st) atomicOr(st, GDN_DEV_TREE);
+            }
+            parent[i] = p;
+        }
+        __syncthreads();
+        // every thread's node: its depth if it is on the accepted path
+        if (tid < N) {
+            bool on = false;
+            int depth = 0;
+            for (int i = node; i > 0; i = parent[i]) on |= i == tid;
+            for (int i = tid; i > 0; i = parent[i]) ++depth;
+            if (tid == node) depth_of_last = depth;
+            const int s = ctx + tid - 1, d = ctx + depth - 1;
+            if (on) {
+                const int32_t *fs = a.table + (size_t)b * a.width + (s >> a.page_shift);
+                const int32_t *fd = a.table + (size_t)b * a.width + (d >> a.page_shift);
+                const int ps = GDN_IN(fs, 4, bt, st) ? *fs : -1, pd = GDN_IN(fd, 4, bt, st) ? *fd : -1;
+                const int mask = (1 << a.page_shift) - 1;
+                const bool okS = ps >= 0 && ps < a.n_pages, okD = pd >= 0 && pd < a.n_pages;
+                if ((!okS || !okD) && blockIdx.x == 0 && st) atomicOr(st, GDN_DEV_PAGE);
+                src_row[depth - 1] = okS ? ((long long)ps * a.h_kv << a.page_shift) + (s & mask) : -1;
+                dst_row[depth - 1] = okD ? ((long long)pd * a.h_kv << a.page_shift) + (d & mask) : -1;
+            }
+        }
+        __syncthreads();
+        if (tid == 0) {  // the path's nodes 1..in_place are where they belong
+            int j = 0;
+            while (j < depth_of_last && src_row[j] == dst_row[j]) ++j;
+            in_place = j;
+        }
+        __syncthreads();
+    }
+    const int k = a.parent ? depth_of_last : node;
+    if (blockIdx.x == 0 && tid == 0) a.ctx_out[b] = ctx + k;
+    if (!a.parent) return;
+    const int first = in_place, rows = k - first;
+    if (rows <= 0) return;
+    const int slices = 2 * a.layers * a.h_kv, parts = gridDim.x;
+    const int s0 = (int)((long long)slices * blockIdx.x / parts), s1 = (int)((long long)slices * (blockIdx.x + 1) / parts);
+    // a round: `group` slices of `cols` units of each row
+    constexpr int kUnits = kCommitThreads * kCommitHold;
+    const int cols = min(a.row_units, kUnits / rows), group = max(1, kUnits / (rows * a.row_units));
+    for (int s = s0; s < s1; s += group)
+        for (int c0 = 0; c0 < a.row_units; c0 += cols) {
+            const int nc = min(cols, a.row_units - c0), ng = min(group, s1 - s), items = ng * rows * nc;
+            uint4 held[kCommitHold];
+#pragma unroll
+            for (int h = 0; h < kCommitHold; ++h) {
+                const int it = tid + h * kCommitThreads;
+                held[h] = make_uint4(0, 0, 0, 0);
+                if (it < items) {
+                    const int col = c0 + it % nc, row = first + it / nc % rows, sl = s + it / (nc * rows);
+                    const int head = sl % a.h_kv, layer = sl / a.h_kv % a.layers, pool = sl / (a.h_kv * a.layers);
+                    const long long r = src_row[row];
+                    if (r >= 0) {
+                        const uint4 *f = (pool ? a.v : a.k) + ((size_t)layer * a.n_pages * a.h_kv << a.page_shift) * a.row_units +
+                                         ((size_t)r + ((size_t)head << a.page_shift)) * a.row_units + col;
+                        if (GDN_IN(f, 16, (Buf{(pool ? a.v : a.k), pool_bytes}), st)) held[h] = *f;
+                    }
+                }
+            }
+            __syncthreads();
+#pragma unroll
+            for (int h = 0; h < kCommitHold; ++h) {
+                const int it = tid + h * kCommitThreads;
+                if (it < items) {
+                    const int col = c0 + it % nc, row = first + it / nc % rows, sl = s + it / (nc * rows);
+                    const int head = sl % a.h_kv, layer = sl / a.h_kv % a.layers, pool = sl / (a.h_kv * a.layers);
+                    const long long r = dst_row[row];
+                    if (r >= 0) {
+                        uint4 *f = (pool ? a.v : a.k) + ((size_t)layer * a.n_pages * a.h_kv << a.page_shift) * a.row_units +
+                                   ((size_t)r + ((size_t)head << a.page_shift)) * a.row_units + col;
+                        if (GDN_IN(f, 16, (Buf{(pool ? a.v : a.k), pool_bytes}), st)) *f = held[h];
+                    }
+                }
+            }
+        }
+}
+
+// ---------------------------------------------------------------- resize, fork
+
+constexpr int kPoolThreads = 1024;
+constexpr int kPoolWarps = kPoolThreads / 32;
+
+// Exclusive prefix sum over the block of one value per thread; total returned.
+__device__ __forceinline__ int block_scan(int v, int &before, int *warp_sum) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(~0u, x, o);
+        if (lane >= o) x += y;
+    }
+    if (lane == 31) warp_sum[warp] = x;
+    __syncthreads();
+    const int w = warp_sum[lane];
+    int s = w;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(~0u, s, o);
+        if (lane >= o) s += y;
+    }
+    const int total = __shfl_sync(~0u, s, 31);
+    before = x - v + __shfl_sync(~0u, s - w, warp);
+    __syncthreads();
+    return total;
+}
+
+// Ids of the first `wanted` free pages, in ascending order, into list; how many
+// there are (at most wanted). Called by the whole block.
+__device__ int find_free(const int32_t *ref, int n_pages, int wanted, int32_t *list, Buf br, Buf bl, int *warp_sum,
+                         int32_t *st) {
+    int found = 0;
+    for (int base = 0; base < n_pages && found < wanted; base += kPoolThreads * 4) {
+        const int i = base + threadIdx.x * 4;
+        int r[4], n = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            r[j] = i + j < n_pages && GDN_IN(ref + i + j, 4, br, st) ? __ldcg(ref + i + j) : 1;
+            n += r[j] == 0;
+        }
+        int at;
+        const int total = block_scan(n, at, warp_sum);
+        at += found;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (r[j] == 0) {
+                if (at < wanted && GDN_IN(list + at, 4, bl, st)) list[at] = i + j;
+                ++at;
+            }
+        found += total;
+    }
+    __syncthreads();
+    return min(found, wanted);
+}
+
+struct ResizeArgs {
+    int batch, width, page_shift, n_pages;
+    const int32_t *want;
+    int32_t *table, *ref, *need, *list, *status;
+};
+
+__global__ void __launch_bounds__(kPoolThreads) resize_pages(ResizeArgs a) {
+    __shared__ int warp_sum[32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    int32_t *st = a.status;
+    const size_t B = a.batch;
+    const Buf bt{a.table, B * (size_t)a.width * 4}, br{a.ref, (size_t)a.n_pages * 4}, bneed{a.need, B * 4},
+        blist{a.list, (size_t)a.n_pages * 4};
+    gdndev::pdl_wait();
+    // one warp per request: entries past the wanted length are given back, the
+    // missing ones below it counted
+    for (int b = warp; b < a.batch; b += kPoolWarps) {
+        const int want = a.want[b];
+        const int keep = want < 0 ? 0 : (int)(((int64_t)want + (1 << a.page_shift) - 1) >> a.page_shift);
+        int missing = 0;
+        if (want >= 0 && keep > a.width) {
+            if (lane == 0 && st) atomicOr(st, GDN_DEV_LENGTH);
+        } else if (want >= 0) {
+            for (int c = lane; c < a.width; c += 32) {
+                int32_t *e = a.table + (size_t)b * a.width + c;
+                const int id = GDN_IN(e, 4, bt, st) ? *e : -1;
+                if (c < keep) {
+                    missing += id < 0;
+                } else if (id >= 0) {
+                    if (id < a.n_pages) {
+                        if (GDN_IN(a.ref + id, 4, br, st)) atomicSub(a.ref + id, 1);
+                    } else if (st) {
+                        atomicOr(st, GDN_DEV_PAGE);
+                    }
+                    if (GDN_IN(e, 4, bt, st)) *e = -1;
+                }
+            }
+#pragma unroll
+            for (int o = 16; o; o >>= 1) missing += __shfl_xor_sync(~0u, missing, o);
+        }
+        if (lane == 0 && GDN_IN(a.need + b, 4, bneed, st)) a.need[b] = missing;
+    }
+    __syncthreads();
+    // where each request's pages begin in the list of taken ones
+    int total = 0;
+    for (int base = 0; base < a.batch; base += kPoolThreads) {
+        const int b = base + tid, n = b < a.batch ? a.need[b] : 0;
+        int at;
+        const int sum = block_scan(n, at, warp_sum);
+        if (b < a.batch) a.need[b] = total + at;
+        total += sum;
+        if (total > a.n_pages) total = a.n_pages + 1;  // more than there can be
+    }
+    __syncthreads();
+    if (total == 0) return;
+    const int found = find_free(a.ref, a.n_pages, min(total, a.n_pages), a.list, br, blist, warp_sum, st);
+    if (found < total && tid == 0 && st) atomicOr(st, GDN_DEV_POOL);
+    for (int b = warp; b < a.batch; b += kPoolWarps) {
+        const int want = a.want[b];
+        const int keep = want < 0 ? 0 : (int)(((int64_t)want + (1 << a.page_shift) - 1) >> a.page_shift);
+        if (keep > a.width) continue;
+        int at = a.need[b];
+        for (int c0 = 0; c0 < keep; c0 += 32) {
+            const int c = c0 + lane;
+            int32_t *e = a.table + (size_t)b * a.width + c;
+            const bool miss = c < keep && GDN_IN(e, 4, bt, st) && *e < 0;
+            const unsigned m = __ballot_sync(~0u, miss);
+            const int k = at + __popc(m & ((1u << lane) - 1));
+            if (miss && k < found) {
+                const int id = a.list[k];
+                *e = id;
+                if (GDN_IN(a.ref + id, 4, br, st)) atomicAdd(a.ref + id, 1);
+            }
+            at += __popc(m);
+        }
+    }
+}
+
+struct ForkArgs {
+    int batch, n_fork, width, page_shift, n_pages, layers, h_kv, row_units;
+    const int32_t *src, *dst;
+    int32_t *table, *ctx, *ref;
+    uint4 *k, *v;
+    int32_t *fresh;  // [n_fork] page taken for the tail; -1 none needed, -2 left out, -3 no page left
+    int32_t *list;
+    int32_t *status;
+};
+
+__global__ void __launch_bounds__(kPoolThreads) fork_take(ForkArgs a) {
+    __shared__ int warp_sum[32];
+    const int tid = threadIdx.x;
+    int32_t *st = a.status;
+    const Buf br{a.ref, (size_t)a.n_pages * 4}, blist{a.list, (size_t)a.n_pages * 4};
+    gdndev::pdl_launch_dependents();
+    gdndev::pdl_wait();
+    int total = 0;
+    for (int base = 0; base < a.n_fork; base += kPoolThreads) {
+        const int i = base + tid;
+        int state = -2;
+        if (i < a.n_fork) {
+            const int s = a.src[i], d = a.dst[i];
+            if (s < 0 || s >= a.batch || d < 0 || d >= a.batch) {
+                if (st) atomicOr(st, GDN_DEV_NODE_RANGE);
+            } else {
+                const int n = a.ctx[s];
+                if (n < 0 || (int64_t)n > (int64_t)a.width << a.page_shift) {
+                    if (st) atomicOr(st, GDN_DEV_LENGTH);
+                } else {
+                    state = (n & ((1 << a.page_shift) - 1)) ? 0 : -1;
+                }
+            }
+        }
+        int at;
+        const int sum = block_scan(state == 0, at, warp_sum);
+        if (i < a.n_fork) a.fresh[i] = state == 0 ? total + at : state;
+        total += sum;
+    }
+    __syncthreads();
+    const int found = total ? find_free(a.ref, a.n_pages, min(total, a.n_pages), a.list, br, blist, warp_sum, st) : 0;
+    if (found < total && tid == 0 && st) atomicOr(st, GDN_DEV_POOL);
+    for (int i = tid; i < a.n_fork; i += kPoolThreads) {
+        int f = a.fresh[i];
+        if (f == -2) continue;
+        if (f >= 0) {
+            f = f < found ? a.list[f] : -3;
+            a.fresh[i] = f;
+            if (f >= 0 && GDN_IN(a.ref + f, 4, br, st)) a.ref[f] = 1;
+        }
+        a.ctx[a.dst[i]] = f == -3 ? 0 : a.ctx[a.src[i]];
+    }
+}
+
+constexpr int kForkThreads = 256;
+
+// grid (parts, n_fork): the table row (first part), and the tail rows of this
+// part's slices (pool, layer, head).
+__global__ void __launch_bounds__(kForkThreads) fork_copy(ForkArgs a) {
+    const int i = blockIdx.y, tid = threadIdx.x;
+    int32_t *st = a.status;
+    const size_t B = a.batch;
+    const Buf bt{a.table, B * (size_t)a.width * 4}, br{a.ref, (size_t)a.n_pages * 4};
+    const size_t slice_units = (size_t)a.row_units << a.page_shift;
+    const size_t pool_bytes = (size_t)a.layers * a.n_pages * a.h_kv * slice_units * 16;
+    gdndev::pdl_wait();
+    const int fresh = a.fresh[i];
+    if (fresh == -2) return;
+    const int s = a.src[i], d = a.dst[i], n = fresh == -3 ? 0 : a.ctx[s];
+    const int full = n >> a.page_shift, tail = n & ((1 << a.page_shift) - 1);
+    const int32_t *from = a.table + (size_t)s * a.width;
+    int32_t *to = a.table + (size_t)d * a.width;
+    for (int c = blockIdx.x * kForkThreads + tid; c < a.width; c += gridDim.x * kForkThreads) {
+        int id = -1;
+        if (c < full) {
+            id = GDN_IN(from + c, 4, bt, st) ? from[c] : -1;
+            if (id >= 0 && id < a.n_pages) {
+                if (GDN_IN(a.ref + id, 4, br, st)) atomicAdd(a.ref + id, 1);
+            } else {
+                id = -1;
+                if (st) atomicOr(st, GDN_DEV_PAGE);
+            }
+        } else if (c == full && fresh >= 0) {
+            id = fresh;
+        }
+        if (GDN_IN(to + c, 4, bt, st)) to[c] = id;
+    }
+    if (fresh < 0) return;
+    const int old = GDN_IN(from + full, 4, bt, st) ? from[full] : -1;
+    const bool known = old >= 0 && old < a.n_pages;
+    if (!known && blockIdx.x == 0 && tid == 0 && st) atomicOr(st, GDN_DEV_PAGE);
+    const int slices = 2 * a.layers * a.h_kv, parts = gridDim.x, units = tail * a.row_units;
+    const long long all = (long long)slices * units;
+    for (long long it = (long long)blockIdx.x * kForkThreads + tid; it < all; it += (long long)parts * kForkThreads) {
+        const int sl = (int)(it / units), u = (int)(it % units);
+        const int head = sl % a.h_kv, layer = sl / a.h_kv % a.layers, pool = sl / (a.h_kv * a.layers);
+        uint4 *base = (pool ? a.v : a.k) + (size_t)layer * a.n_pages * a.h_kv * slice_units;
+        const uint4 *f = base + ((size_t)old * a.h_kv + head) * slice_units + u;
+        uint4 *t = base + ((size_t)fresh * a.h_kv + head) * slice_units + u;
+        const Buf bpool{(pool ? a.v : a.k), pool_bytes};
+        const uint4 v = known && GDN_IN(f, 16, bpool, st) ? *f : make_uint4(0, 0, 0, 0);
+        if (GDN_IN(t, 16, bpool, st)) *t = v;
+    }
+}
+
+int page_shift(int page_tokens) {
+    int s = 0;
+    while ((1 << s) < page_tokens) ++s;
+    return s;
+}
+
+int parts_for(int requests, int most) {
+    const int sms = gdnhost::sm_count();
+    const int want = (4 * (sms > 0 ? sms : 152) + requests - 1) / requests;
+    return want < 1 ? 1 : want < most ? want : most;
+}
+
+constexpr size_t round256(size_t n) { return (n + 255) / 256 * 256; }
+
+}  // namespace
+
+extern "C" int kv_commit_path(const attn_dims *dims, int32_t n_nodes, const int32_t *parent_dev,
+                              const int32_t *accept_node, const int32_t *ctx_len, const int32_t *page_table,
+                              void *k_pages, void *v_pages, int32_t *ctx_out, int32_t *dev_status,
+                              gdn_stream_t stream) {
+    if (const int rc = gdnhost::check_attn(dims)) return rc;
+    if (n_nodes < 2 || n_nodes > kMaxNodes) return GDN_ERR_DIMS;
+    if (!accept_node || !ctx_len || !ctx_out || (parent_dev && (!page_table || !k_pages || !v_pages))) return GDN_ERR_NULL;
+    using gdnhost::aligned_to;
+    if (!aligned_to(k_pages, 16) || !aligned_to(v_pages, 16)) return GDN_ERR_ALIGN;
+    for (const void *p : {(const void *)parent_dev, (const void *)accept_node, (const void *)ctx_len,
+                          (const void *)page_table, (const void *)ctx_out, (const void *)dev_status})
+        if (!aligned_to(p, 4)) return GDN_ERR_ALIGN;
+    CommitArgs a{n_nodes, dims->layers, dims->h_kv, page_shift(dims->page_tokens), dims->n_pages, dims->table_width,
+                 (int)(dims->d_head * gdnhost::attn_elem_bytes(dims) / 16), parent_dev, accept_node, ctx_len, page_table,
+                 static_cast<uint4 *>(k_pages), static_cast<uint4 *>(v_pages), ctx_out, dev_status};
+    const int64_t slices = 2LL * dims->layers * dims->h_kv;
+    const int parts = parent_dev ? parts_for(dims->batch, slices < 65535 ? (int)slices : 65535) : 1;
+    return gdndev::launch_pdl(commit_path, dim3(parts, dims->batch), dim3(kCommitThreads), 0,
+                              static_cast<cudaStream_t>(stream), a) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+
+extern "C" size_t kv_pages_workspace_bytes(const attn_dims *dims) {
+    if (gdnhost::check_attn(dims)) return 0;
+    return round256((size_t)dims->batch * 4) + round256((size_t)dims->n_pages * 4);
+}
+
+static int check_pages(const attn_dims *dims, std::initializer_list<const void *> ints, void *workspace,
+                       size_t workspace_bytes, const void *dev_status) {
+    if (const int rc = gdnhost::check_attn(dims)) return rc;
+    for (const void *p : ints)
+        if (!p) return GDN_ERR_NULL;
+    for (const void *p : ints)
+        if (!gdnhost::aligned_to(p, 4)) return GDN_ERR_ALIGN;
+    if (!gdnhost::aligned_to(dev_status, 4)) return GDN_ERR_ALIGN;
+    if (!workspace || workspace_bytes < kv_pages_workspace_bytes(dims) || !gdnhost::aligned_to(workspace, 256))
+        return GDN_ERR_WORKSPACE;
+    return GDN_OK;
+}
+
+extern "C" int kv_pages_resize(const attn_dims *dims, const int32_t *want, int32_t *page_table, int32_t *page_ref,
+                               void *workspace, size_t workspace_bytes, int32_t *dev_status, gdn_stream_t stream) {
+    if (const int rc = check_pages(dims, {want, page_table, page_ref}, workspace, workspace_bytes, dev_status)) return rc;
+    int32_t *need = static_cast<int32_t *>(workspace);
+    int32_t *list = reinterpret_cast<int32_t *>(static_cast<char *>(workspace) + round256((size_t)dims->batch * 4));
+    ResizeArgs a{dims->batch, dims->table_width, page_shift(dims->page_tokens), dims->n_pages, want, page_table, page_ref,
+                 need, list, dev_status};
+    return gdndev::launch_pdl(resize_pages, dim3(1), dim3(kPoolThreads), 0, static_cast<cudaStream_t>(stream), a) ==
+                   cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+
+extern "C" int kv_pages_fork(const attn_dims *dims, int32_t n_fork, const int32_t *src, const int32_t *dst,
+                             int32_t *page_table, int32_t *ctx_len, int32_t *page_ref, void *k_pages, void *v_pages,
+                             void *workspace, size_t workspace_bytes, int32_t *dev_status, gdn_stream_t stream) {
+    if (const int rc = gdnhost::check_attn(dims)) return rc;
+    if (n_fork < 1 || n_fork > dims->batch) return GDN_ERR_DIMS;
+    if (!k_pages || !v_pages) return GDN_ERR_NULL;
+    if (const int rc = check_pages(dims, {src, dst, page_table, ctx_len, page_ref}, workspace, workspace_bytes, dev_status))
+        return rc;
+    if (!gdnhost::aligned_to(k_pages, 16) || !gdnhost::aligned_to(v_pages, 16)) return GDN_ERR_ALIGN;
+    int32_t *fresh = static_cast<int32_t *>(workspace);
+    int32_t *list = reinterpret_cast<int32_t *>(static_cast<char *>(workspace) + round256((size_t)dims->batch * 4));
+    ForkArgs a{dims->batch, n_fork, dims->table_width, page_shift(dims->page_tokens), dims->n_pages, dims->layers,
+               dims->h_kv, (int)(dims->d_head * gdnhost::attn_elem_bytes(dims) / 16), src, dst, page_table, ctx_len,
+               page_ref, static_cast<uint4 *>(k_pages), static_cast<uint4 *>(v_pages), fresh, list, dev_status};
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (gdndev::launch_pdl(fork_take, dim3(1), dim3(kPoolThreads), 0, s, a) != cudaSuccess) return GDN_ERR_CUDA;
+    const int64_t slices = 2LL * dims->layers * dims->h_kv;
+    const int parts = parts_for(n_fork, slices < 65535 ? (int)slices : 65535);
+    return gdndev::launch_pdl(fork_copy, dim3(parts, n_fork), dim3(kForkThreads), 0, s, a) == cudaSuccess ? GDN_OK
+                                                                                                      : GDN_ERR_CUDA;
+}
