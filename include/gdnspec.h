@@ -524,7 +524,8 @@ int attn_qk_norm_rope(const attn_dims *dims, int32_t n_tok, const void *qkv, int
  *              GDN_DEV_TREE and taken as i - 1
  * bf16: products on the tensor cores with f32 accumulation, softmax in f32, its
  * weights rounded to bf16 for the second product; f32: all in f32.
- * Limits: 1 <= n_tok <= GDN_MAX_TOKENS, batch * h_kv <= 65535, scale finite.
+ * Limits: 1 <= n_tok <= GDN_MAX_TOKENS, batch * h_kv <= 65535,
+ * scale finite and above 0.
  * Returns GDN_OK or GDN_ERR_{NULL,DIMS,ALIGN,DTYPE,TREE_*,WORKSPACE,CUDA}.
  */
 int attn_verify_span(const attn_dims *dims, int32_t n_tok, const void *q, const void *k_pages,

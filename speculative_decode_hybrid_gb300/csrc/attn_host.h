@@ -9,7 +9,12 @@ namespace gdnattn {
 
 struct AttnArgs;
 
+// f32 arithmetic (attn_simt.cu).
 size_t simt_workspace(const attn_dims *d, int n_tok);
 int simt_launch(const attn_dims *d, const AttnArgs &a, void *workspace, cudaStream_t st);
+
+// bf16 on the tensor cores (attn_tc.cu).
+size_t tc_workspace(const attn_dims *d, int n_tok);
+int tc_launch(const attn_dims *d, const AttnArgs &a, void *workspace, cudaStream_t st);
 
 }  // namespace gdnattn

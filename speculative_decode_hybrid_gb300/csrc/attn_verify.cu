@@ -14,7 +14,7 @@ namespace {
 int attend(const attn_dims *dims, int32_t n_tok, const int32_t *parent_dev, const void *q, const void *k_pages,
            const void *v_pages, const int32_t *page_table, const int32_t *ctx_len, float scale, void *out,
            void *workspace, size_t workspace_bytes, int32_t *dev_status, gdn_stream_t stream) {
-    if (!std::isfinite(scale)) return GDN_ERR_DIMS;
+    if (!std::isfinite(scale) || scale <= 0.f) return GDN_ERR_DIMS;
     if (!q || !k_pages || !v_pages || !page_table || !ctx_len || !out) return GDN_ERR_NULL;
     for (const void *p : {q, k_pages, v_pages, (const void *)out})
         if (!gdnhost::aligned_to(p, 16)) return GDN_ERR_ALIGN;
@@ -27,7 +27,8 @@ int attend(const attn_dims *dims, int32_t n_tok, const int32_t *parent_dev, cons
     const gdnattn::AttnArgs a{dims->batch, n_tok, dims->h_q, dims->h_kv, dims->d_head, shift, dims->n_pages,
                               dims->table_width, scale * gdnattn::kLog2e, q, k_pages, v_pages, page_table, ctx_len,
                               parent_dev, out, dev_status};
-    return gdnattn::simt_launch(dims, a, workspace, static_cast<cudaStream_t>(stream));
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return dims->in_dtype == GDN_BF16 ? gdnattn::tc_launch(dims, a, workspace, st) : gdnattn::simt_launch(dims, a, workspace, st);
 }
 
 int check(const attn_dims *dims, int32_t n_tok) {
@@ -39,7 +40,8 @@ int check(const attn_dims *dims, int32_t n_tok) {
 }  // namespace
 
 extern "C" size_t attn_workspace_bytes(const attn_dims *dims, int32_t n_tok) {
-    return check(dims, n_tok) ? 0 : gdnattn::simt_workspace(dims, n_tok);
+    if (check(dims, n_tok)) return 0;
+    return dims->in_dtype == GDN_BF16 ? gdnattn::tc_workspace(dims, n_tok) : gdnattn::simt_workspace(dims, n_tok);
 }
 
 extern "C" int attn_verify_span(const attn_dims *dims, int32_t n_tok, const void *q, const void *k_pages,
