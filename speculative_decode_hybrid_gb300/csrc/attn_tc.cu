@@ -16,7 +16,7 @@
 //
 // Warps: 4 per M tile for the softmax, one that keeps the TMA loads of the next
 // tiles in flight (a page's rows of one head are a box of a 3-d tensor map, so
-// a tile is gathered page by page), one that issues the products.
+// a tile is gathered page by page), one that issues each of the products.
 //
 // Work is split over the whole flattened list of (request, head, M tiles, slot
 // tile): block i of n takes the i-th n-th of it, whatever the requests'
@@ -43,21 +43,36 @@ using gdndev::Buf;
 constexpr int kM = 128;                    // rows of an M tile
 constexpr unsigned long long kGiveUpNs = 1000000000ull;  // a wait's limit
 
-// Smallest power of two of tensor-memory columns: all 512, one block per SM.
-constexpr int kTmemCols = 512;
+constexpr int kTmemCols = 512;  // all of an SM's: one block per SM
+constexpr int kMaxBlocks = 160, kNotes = 2 * kMaxBlocks / 32;
 
 template <int D, int W>
 struct Shape {
     static constexpr int kN = D == 256 ? 64 : 128;       // slots of a tile
     static constexpr int kChunks = D / 64;               // 128-byte column chunks of a row
-    static constexpr int kStages = D == 64 ? 4 : D == 128 && W == 1 ? 3 : 2;
-    static constexpr unsigned kTileBytes = kN * D * 2;   // of K, and of V
-    static constexpr unsigned kQBytes = kM * D * 2;      // of one M tile
     static constexpr int kSlots = 2;                     // S buffers: one per M tile, or two in turn
-    static constexpr int kThreads = W * 128 + 64;
-    static constexpr unsigned kSmem = W * kQBytes + 2 * kStages * kTileBytes + 1024;
-    static_assert(W * D + kSlots * kN <= kTmemCols, "tensor memory");
+    static constexpr unsigned kSCol = W * D, kQCol = kSCol + kSlots * kN;  // tensor-memory columns: O, S, Q
+    // Q is read from tensor memory where it fits beside O and S: a product then
+    // reads half as much shared memory
+    static constexpr bool kQInTmem = kQCol + W * D / 2 <= kTmemCols;
+    static constexpr int kStages = D == 64 ? 6 : kQInTmem ? 3 : 2;
+    static constexpr unsigned kTileBytes = kN * D * 2;   // of K, and of V
+    static constexpr unsigned kQBytes = kQInTmem ? 0 : kM * D * 2;  // of one M tile in shared memory
+    static constexpr unsigned kPassBytes = kQInTmem ? W * 4 * 4096 : 0;  // a warp's 32 rows x 128 bytes of Q on their way
+    static constexpr int kThreads = W * 128 + 96;
+    static constexpr unsigned kSmem = W * kQBytes + 2 * kStages * kTileBytes + kPassBytes + 1024;
+    static_assert(kQCol <= kTmemCols, "tensor memory");
 };
+
+// What the host works out: divisions take a warp longer than a load from L2.
+struct Plan {
+    int group, rows;        // query heads of a key/value head; rows of one key/value head
+    int m_groups, units;    // groups of W M tiles of a head; units (head, group) of a request
+    int blocks;
+    unsigned by_group, by_m_groups, by_blocks;  // 2^32 / n rounded up: x / n for x * n < 2^32
+};
+
+__device__ __forceinline__ int quotient(int x, unsigned by) { return by ? (int)__umulhi((unsigned)x, by) : x; }  // by 1: 2^32 is 0
 
 struct Work {
     int b, off, left;  // request, tiles of it already dealt out, tiles of this block still to come
@@ -68,7 +83,7 @@ struct Segment {
 };
 
 template <int kN>
-__device__ __forceinline__ Segment next_segment(const AttnArgs &a, int units, Work &w) {
+__device__ __forceinline__ Segment next_segment(const AttnArgs &a, const Plan &plan, Work &w) {
     Segment s;
     s.b = w.b;
     s.slots = gdnattn::slots_of(a, w.b);
@@ -79,21 +94,59 @@ __device__ __forceinline__ Segment next_segment(const AttnArgs &a, int units, Wo
     s.n = min(s.tiles - s.tile0, w.left);
     w.off += s.n;
     w.left -= s.n;
-    if (w.off == s.tiles * units) ++w.b, w.off = 0;
+    if (w.off == s.tiles * plan.units) ++w.b, w.off = 0;
     return s;
 }
 
-// Tiles of all requests before `upto`, times the units of one: by one warp.
-template <int kN>
-__device__ __forceinline__ long long tiles_before(const AttnArgs &a, int units, int upto) {
-    long long n = 0;
-    for (int b = threadIdx.x & 31; b < upto; b += 32) n += (gdnattn::slots_of(a, b) + kN - 1) / kN;
-#pragma unroll
-    for (int o = 16; o; o >>= 1) n += __shfl_xor_sync(~0u, n, o);
-    return n * units;
-}
+// Block i's share of `total` tiles begins at total * i / blocks, rounded down.
+struct Share {
+    long long whole;
+    int rest;
+    __device__ __forceinline__ Share(long long total, int blocks) {
+        if (total >> 31 == 0)  // the 64-bit division takes long, and totals are small
+            whole = (unsigned)total / (unsigned)blocks;
+        else
+            whole = total / blocks;
+        rest = (int)(total - whole * blocks);
+    }
+    __device__ __forceinline__ long long start(int i, const Plan &plan) const {
+        return whole * i + quotient(rest * i, plan.by_blocks);
+    }
+};
 
-__device__ __forceinline__ long long range_start(long long total, int block, int blocks) { return total * block / blocks; }
+// This block's share, and the request in which it begins: by each warp for
+// itself, so that none waits for another.
+template <int kN>
+__device__ __forceinline__ Work block_work(const AttnArgs &a, const Plan &plan, bool flag) {
+    const int lane = threadIdx.x & 31;
+    auto tiles_of = [&](int b) { return b < a.batch ? (gdnattn::slots_of(a, b) + kN - 1) / kN : 0; };
+    const int mine = tiles_of(lane);
+    long long total = 0;
+    for (int b0 = 0; b0 < a.batch; b0 += 32) total += __reduce_add_sync(~0u, b0 ? tiles_of(b0 + lane) : mine);
+    const int units = plan.units;
+    const Share share(total * units, plan.blocks);
+    const long long lo = share.start(blockIdx.x, plan), hi = share.start(blockIdx.x + 1, plan);
+    Work w{0, 0, 0};
+    long long before = 0;
+    for (int b0 = 0; b0 < a.batch && (lo >= before || flag); b0 += 32) {
+        const int b = b0 + lane, n = b0 ? tiles_of(b) : mine;
+        int x = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(~0u, x, o);
+            if (lane >= o) x += y;
+        }
+        const long long first = before + (long long)(x - n) * units;
+        const unsigned here = __ballot_sync(~0u, lo >= first && lo < first + (long long)n * units);
+        if (here) {
+            const int from = __ffs(here) - 1;
+            w = {b0 + from, (int)(lo - __shfl_sync(~0u, first, from)), (int)(hi - lo)};
+        }
+        if (flag && a.status && b < a.batch && n == 0) atomicOr(a.status, GDN_DEV_LENGTH);
+        before += (long long)__shfl_sync(~0u, x, 31) * units;
+    }
+    return w;
+}
 
 __device__ __forceinline__ unsigned saddr(const void *p) { return (unsigned)__cvta_generic_to_shared(p); }
 __device__ __forceinline__ void bar_init(unsigned bar, unsigned count) {
@@ -171,18 +224,25 @@ __device__ __forceinline__ unsigned seen32(int rel, unsigned long long path) {
     return ((unsigned)path << -rel) | ((1u << -rel) - 1u);
 }
 
+// Row r of a key/value head's product in q and out, in heads: node r / group, the
+// group's query head r % group.
+__device__ __forceinline__ size_t row_offset(const AttnArgs &a, const Plan &plan, int b, int kv, int r) {
+    const int t = quotient(r, plan.by_group);
+    return ((size_t)b * a.n_tok + t) * a.h_q + (kv - t) * plan.group + r;
+}
+
 struct Pieces {
     float4 *o;    // [2 blocks][D / 4][W * 128]
     float2 *ms;   // [2 blocks][W * 128]: reference maximum in powers of two, sum
+    int *unit;    // [2 blocks]: request * units + unit of a block's first and last piece of a shared unit, -1 for none
 };
 
 template <int D, int W>
 struct Control {
     static constexpr int kStages = Shape<D, W>::kStages;
     unsigned long long k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
-    unsigned long long s_full[2], p_full[2], pv_done[2], q_full, drain;
+    unsigned long long s_full[2], p_full[2], pv_done[2], q_full, drain[2];
     unsigned long long odd_nodes[4];  // drafted nodes with a value of v that is no number, by segment
-    Work work;
     unsigned tmem;
     int quit;
 };
@@ -190,20 +250,19 @@ struct Control {
 template <int D, int W>
 __global__ void __launch_bounds__(Shape<D, W>::kThreads, 1)
 attend(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
-       const __grid_constant__ AttnArgs a, const __grid_constant__ Pieces pieces) {
+       const __grid_constant__ AttnArgs a, const __grid_constant__ Plan plan, const __grid_constant__ Pieces pieces) {
     using S = Shape<D, W>;
     constexpr int kN = S::kN, kStages = S::kStages;
     extern __shared__ char raw[];
     __shared__ Control<D, W> c;
     char *base = raw + ((1024 - (saddr(raw) & 1023)) & 1023);
-    const unsigned q_s = saddr(base), k_s = q_s + W * S::kQBytes, v_s = k_s + kStages * S::kTileBytes;
+    const unsigned q_s = saddr(base), k_s = q_s + W * S::kQBytes, v_s = k_s + kStages * S::kTileBytes, pass_s = v_s + kStages * S::kTileBytes;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int group = a.h_q / a.h_kv, rows = a.n_tok * group;
-    const int m_groups = (rows + W * kM - 1) / (W * kM), units = a.h_kv * m_groups;
+    const int group = plan.group, rows = plan.rows;
     int32_t *st = a.status;
-    constexpr int kTmaWarp = W * 4, kMmaWarp = W * 4 + 1;
+    constexpr int kTmaWarp = W * 4, kScoreWarp = W * 4 + 1, kSumWarp = W * 4 + 2;
 
-    if (warp == kMmaWarp) gdntc::tmem_alloc<kTmemCols>(&c.tmem);
+    if (warp == kScoreWarp) gdntc::tmem_alloc<kTmemCols>(&c.tmem);
     if (tid == 0) {
         for (int i = 0; i < kStages; ++i) {
             bar_init(saddr(&c.k_full[i]), 1);
@@ -217,44 +276,22 @@ attend(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtens
             bar_init(saddr(&c.pv_done[i]), 1);
         }
         bar_init(saddr(&c.q_full), W * 4);
-        bar_init(saddr(&c.drain), 1);
+        bar_init(saddr(&c.drain[0]), 1);
+        bar_init(saddr(&c.drain[1]), 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         c.quit = 0;
         for (int i = 0; i < 4; ++i) c.odd_nodes[i] = 0;
-    }
-    gdndev::pdl_launch_dependents();
-    gdndev::pdl_wait();
-    if (warp == 0) {
-        // this block's share of the list, and the request in which it begins
-        const long long total = tiles_before<kN>(a, units, a.batch);
-        const long long lo = range_start(total, blockIdx.x, gridDim.x), hi = range_start(total, blockIdx.x + 1, gridDim.x);
-        long long before = 0;
-        for (int b0 = 0; b0 < a.batch; b0 += 32) {
-            const int b = b0 + lane;
-            const long long n = b < a.batch ? (long long)((gdnattn::slots_of(a, b) + kN - 1) / kN) * units : 0;
-            long long x = n;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const long long y = __shfl_up_sync(~0u, x, o);
-                if (lane >= o) x += y;
-            }
-            if (lo >= before + x - n && lo < before + x) c.work = {b, (int)(lo - (before + x - n)), (int)(hi - lo)};
-            before += __shfl_sync(~0u, x, 31);
-            if (lo < before) break;
-        }
-        if (lane == 0 && hi == lo) c.work = {0, 0, 0};
-        if (blockIdx.x == 0 && st)
-            for (int b = lane; b < a.batch; b += 32)
-                if (gdnattn::slots_of(a, b) == 0) atomicOr(st, GDN_DEV_LENGTH);
     }
     gdntc::fence_before_sync();
     __syncthreads();
     gdntc::fence_after_sync();
     const unsigned tmem = c.tmem;
-    Work work = c.work;
+    gdndev::pdl_launch_dependents();
+    gdndev::pdl_wait();
+    Work work = block_work<kN>(a, plan, blockIdx.x == 0 && warp == 0);
+    if (tid == 0) pieces.unit[2 * blockIdx.x] = pieces.unit[2 * blockIdx.x + 1] = -1;
     volatile int *quit = &c.quit;
-    // tensor-memory columns: O of each M tile, then the S buffers
-    constexpr unsigned kSCol = W * D;
+    constexpr unsigned kSCol = S::kSCol, kQCol = S::kQCol;
 
     if (warp == kTmaWarp) {
         int g = 0;  // tiles so far
@@ -264,8 +301,8 @@ attend(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtens
         const Buf bt{a.table, (size_t)a.batch * a.width * 4};
         bool ok = true;
         while (work.left > 0 && ok) {
-            const Segment s = next_segment<kN>(a, units, work);
-            const int kv = s.unit / m_groups;
+            const Segment s = next_segment<kN>(a, plan, work);
+            const int kv = quotient(s.unit, plan.by_m_groups);
             const int32_t *row = a.table + (size_t)s.b * a.width;
             const int32_t *e = row + ((s.tile0 * kN + mine * page_rows) >> a.page_shift);
             // a page id is read one tile ahead
@@ -310,66 +347,77 @@ attend(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtens
                 }
             }
         }
-    } else if (warp == kMmaWarp) {
+    } else if (warp == kScoreWarp) {
+        // S = Q K^T. The sums have a warp of their own: each waits for its inputs
+        // while the other's products run.
         if (lane == 0) {
-            constexpr unsigned kIdS = gdntc::idesc_bf16(kM, kN, false), kIdO = gdntc::idesc_bf16(kM, D, true);
+            constexpr unsigned kIdS = gdntc::idesc_bf16(kM, kN, false);
             int g = 0;
             unsigned seg = 0;
             bool ok = true;
-            auto scores = [&](int tile, int w, int slot) {  // S = Q K^T of one M tile
-                const unsigned k = k_s + (tile % kStages) * S::kTileBytes, q = q_s + w * S::kQBytes;
-#pragma unroll
-                for (int i = 0; i < D / 16; ++i)
-                    gdntc::mma_bf16_ss(tmem + kSCol + slot * kN, gdntc::smem_desc_sw128(q + (i / 4) * (kM * 128) + (i % 4) * 32),
-                                       gdntc::smem_desc_sw128(k + (i / 4) * (kN * 128) + (i % 4) * 32), kIdS, i > 0);
-                gdntc::mma_commit(saddr(&c.s_full[slot]));
-            };
-            auto sums = [&](int tile, int w, int slot, bool first) {  // O += P V
-                const unsigned v = v_s + (tile % kStages) * S::kTileBytes;
-#pragma unroll
-                for (int i = 0; i < kN / 16; ++i)
-                    gdntc::mma_bf16_ts(tmem + w * D, tmem + kSCol + slot * kN + i * 8,
-                                       gdntc::smem_desc_sw128_mn(v + i * 2048, kN * 128), kIdO, !first || i > 0);
-                gdntc::mma_commit(saddr(&c.pv_done[slot]));
-            };
-            auto k_ready = [&](int tile) { return wait(saddr(&c.k_full[tile % kStages]), (tile / kStages) & 1, quit); };
-            auto v_ready = [&](int tile) { return wait(saddr(&c.v_full[tile % kStages]), (tile / kStages) & 1, quit); };
             while (work.left > 0 && ok) {
-                const Segment s = next_segment<kN>(a, units, work);
-                ok = wait(saddr(&c.q_full), seg & 1, quit) && k_ready(g);
+                const Segment s = next_segment<kN>(a, plan, work);
+                ok = wait(saddr(&c.q_full), seg & 1, quit);
                 ++seg;
-                if (!ok) break;
                 gdntc::fence_after_sync();
-                for (int w = 0; w < W; ++w) scores(g, w, W == 2 ? w : g & 1);
-                gdntc::mma_commit(saddr(&c.k_empty[g % kStages]));
                 for (int j = 0; j < s.n && ok; ++j, ++g) {
-                    const bool more = j + 1 < s.n;
-                    if (W == 1 && more) {
-                        ok = k_ready(g + 1);
-                        if (!ok) break;
-                        gdntc::fence_after_sync();
-                        scores(g + 1, 0, (g + 1) & 1);
-                        gdntc::mma_commit(saddr(&c.k_empty[(g + 1) % kStages]));
-                    }
-                    for (int w = 0; w < W; ++w) {
+                    const int stage = g % kStages;
+                    const unsigned k = k_s + stage * S::kTileBytes;
+                    ok = wait(saddr(&c.k_full[stage]), (g / kStages) & 1, quit);
+                    for (int w = 0; w < W && ok; ++w) {
                         const int slot = W == 2 ? w : g & 1;
-                        ok = wait(saddr(&c.p_full[slot]), W == 2 ? g & 1 : (g >> 1) & 1, quit) && (w > 0 || v_ready(g));
+                        // the weights that lay in this S buffer have been used
+                        if (W == 2 && g >= 1) ok = wait(saddr(&c.pv_done[w]), (g - 1) & 1, quit);
+                        if (W == 1 && g >= 2) ok = wait(saddr(&c.pv_done[slot]), ((g - 2) >> 1) & 1, quit);
                         if (!ok) break;
                         gdntc::fence_after_sync();
-                        sums(g, w, slot, j == 0);
-                        if (w == W - 1) gdntc::mma_commit(saddr(&c.v_empty[g % kStages]));
-                        if (W == 2 && more) {
-                            if (w == 0) ok = k_ready(g + 1);
-                            if (!ok) break;
-                            if (w == 0) gdntc::fence_after_sync();
-                            scores(g + 1, w, w);
-                            if (w == 1) gdntc::mma_commit(saddr(&c.k_empty[(g + 1) % kStages]));
+#pragma unroll
+                        for (int i = 0; i < D / 16; ++i) {
+                            const uint64_t kd = gdntc::smem_desc_sw128(k + (i / 4) * (kN * 128) + (i % 4) * 32);
+                            if constexpr (S::kQInTmem)
+                                gdntc::mma_bf16_ts(tmem + kSCol + slot * kN, tmem + kQCol + w * (D / 2) + i * 8, kd, kIdS, i > 0);
+                            else
+                                gdntc::mma_bf16_ss(tmem + kSCol + slot * kN,
+                                                   gdntc::smem_desc_sw128(q_s + w * S::kQBytes + (i / 4) * (kM * 128) + (i % 4) * 32),
+                                                   kd, kIdS, i > 0);
                         }
+                        gdntc::mma_commit(saddr(&c.s_full[slot]));
+                        if (w == W - 1) gdntc::mma_commit(saddr(&c.k_empty[stage]));
                     }
                 }
             }
-            gdntc::mma_commit(saddr(&c.drain));
-            wait(saddr(&c.drain), 0, nullptr);  // no product may run on when the columns are freed
+            gdntc::mma_commit(saddr(&c.drain[0]));
+            wait(saddr(&c.drain[0]), 0, nullptr);  // no product may run on when the columns are freed
+        }
+        __syncwarp();
+    } else if (warp == kSumWarp) {
+        // O += P V
+        if (lane == 0) {
+            constexpr unsigned kIdO = gdntc::idesc_bf16(kM, D, true);
+            int g = 0;
+            bool ok = true;
+            while (work.left > 0 && ok) {
+                const Segment s = next_segment<kN>(a, plan, work);
+                for (int j = 0; j < s.n && ok; ++j, ++g) {
+                    const int stage = g % kStages;
+                    const unsigned v = v_s + stage * S::kTileBytes;
+                    ok = wait(saddr(&c.v_full[stage]), (g / kStages) & 1, quit);
+                    for (int w = 0; w < W && ok; ++w) {
+                        const int slot = W == 2 ? w : g & 1;
+                        ok = wait(saddr(&c.p_full[slot]), W == 2 ? g & 1 : (g >> 1) & 1, quit);
+                        if (!ok) break;
+                        gdntc::fence_after_sync();
+#pragma unroll
+                        for (int i = 0; i < kN / 16; ++i)
+                            gdntc::mma_bf16_ts(tmem + w * D, tmem + kSCol + slot * kN + i * 8,
+                                               gdntc::smem_desc_sw128_mn(v + i * 2048, kN * 128), kIdO, j > 0 || i > 0);
+                        gdntc::mma_commit(saddr(&c.pv_done[slot]));
+                        if (w == W - 1) gdntc::mma_commit(saddr(&c.v_empty[stage]));
+                    }
+                }
+            }
+            gdntc::mma_commit(saddr(&c.drain[1]));
+            wait(saddr(&c.drain[1]), 0, nullptr);
         }
         __syncwarp();
     } else {
@@ -377,6 +425,7 @@ attend(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtens
         const unsigned lane_addr = (unsigned)(warp & 3) << 21;  // 32 lanes each, in bits 16 and up
         const Buf bq{a.q, (size_t)a.batch * a.n_tok * a.h_q * D * 2}, bout{a.out, (size_t)a.batch * a.n_tok * a.h_q * D * 2},
             bpar{a.parent, (size_t)a.batch * (a.n_tok + 1) * 4};
+        constexpr int kBatch = W == 2 ? 1 : S::kChunks;  // column chunks of Q loaded at once: as the registers allow
         const float scale = a.scale_log2;
         // With one M tile the scores of tile g are issued before the sums of g - 1,
         // so a tile's scores only tell that the sums of g - 2 are done: a barrier
@@ -389,30 +438,75 @@ attend(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtens
         bool ok = true;
         while (work.left > 0 && ok) {
             const bool first_segment = seg == 0;
-            const Segment s = next_segment<kN>(a, units, work);
-            const int kv = s.unit / m_groups, row0 = (s.unit % m_groups) * W * kM + w * kM, row = row0 + row_in_tile;
+            const Segment s = next_segment<kN>(a, plan, work);
+            const int kv = quotient(s.unit, plan.by_m_groups), row0 = ((s.unit - kv * plan.m_groups) * W + w) * kM, row = row0 + row_in_tile;
             const int ctx = s.slots - a.n_tok;
-            // the M tile's queries, swizzled as the descriptors say; the scores of
-            // the segment before have been read, so their products are done with q
-            for (int i = row_in_tile; i < kM * (D / 8); i += 128) {
-                const int r = i / (D / 8), u = i % (D / 8), qr = row0 + r;
-                uint4 x = make_uint4(0, 0, 0, 0);
-                if (qr < rows) {
-                    const uint4 *f = reinterpret_cast<const uint4 *>(
-                        static_cast<const __nv_bfloat16 *>(a.q) +
-                        (((size_t)s.b * a.n_tok + qr / group) * a.h_q + kv * group + qr % group) * D) + u;
-                    if (GDN_IN(f, 16, bq, st)) x = *f;
-                }
-                *reinterpret_cast<uint4 *>(base + w * S::kQBytes + (u / 8) * (kM * 128) + r * 128 + (((u % 8) ^ (r % 8)) * 16)) = x;
+            // the M tile's queries: a warp's 32 rows, eight lanes to 128 bytes of a
+            // row; the scores of the segment before have been read, so their
+            // products are done with them
+            const bool live = row < rows, warp_live = row0 + (warp & 3) * 32 < rows;
+            auto row_at = [&](int r) { return row_offset(a, plan, s.b, kv, r) * D; };
+            const size_t q_row = live ? row_at(row) : 0;
+            const uint4 *from[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int r = row0 + (warp & 3) * 32 + i * 4 + lane / 8;
+                from[i] = r < rows ? reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q) + row_at(r)) + lane % 8
+                                   : nullptr;
             }
-            gdntc::fence_smem_to_async();
+#pragma unroll
+            for (int k0 = 0; k0 < S::kChunks; k0 += kBatch) {
+                uint4 x[kBatch][8];
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        x[k][i] = make_uint4(0, 0, 0, 0);
+                        if (from[i] && GDN_IN(from[i] + (k0 + k) * 8, 16, bq, st)) x[k][i] = from[i][(k0 + k) * 8];
+                    }
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k) {
+                    // rows of 128 bytes, 16-byte units swizzled: in shared memory as the
+                    // descriptors want them, or on the way to tensor memory
+                    char *to = S::kQInTmem ? base + (pass_s - q_s) + warp * 4096
+                                           : base + w * S::kQBytes + (k0 + k) * (kM * 128) + (warp & 3) * 4096;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int r = i * 4 + lane / 8;
+                        *reinterpret_cast<uint4 *>(to + r * 128 + (lane % 8 ^ r % 8) * 16) = x[k][i];
+                    }
+                    if constexpr (S::kQInTmem) {
+                        __syncwarp();
+                        unsigned y[32];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const uint4 u = *reinterpret_cast<const uint4 *>(to + lane * 128 + (i ^ lane % 8) * 16);
+                            y[4 * i] = u.x, y[4 * i + 1] = u.y, y[4 * i + 2] = u.z, y[4 * i + 3] = u.w;
+                        }
+                        gdntc::tmem_st32(tmem + lane_addr + kQCol + w * (D / 2) + (k0 + k) * 32, y);
+                        __syncwarp();
+                    }
+                }
+            }
+            if constexpr (S::kQInTmem) {
+                gdntc::tmem_wait_st();
+                gdntc::fence_before_sync();
+            } else {
+                gdntc::fence_smem_to_async();
+            }
+            if (work.left > 0) {  // the next segment's queries on their way to L2
+                Work peek = work;
+                const Segment n = next_segment<kN>(a, plan, peek);
+                const int nkv = quotient(n.unit, plan.by_m_groups), r = ((n.unit - nkv * plan.m_groups) * W + w) * kM + row_in_tile;
+                if (r < rows)
+                    gdndev::prefetch_l2_range(static_cast<const __nv_bfloat16 *>(a.q) + row_offset(a, plan, n.b, nkv, r) * D, D * 2, 0, 1);
+            }
             if (w == 0 && row_in_tile == 0) c.odd_nodes[(seg + 1) & 3] = 0;
             __syncwarp();
             if (lane == 0) bar_arrive(saddr(&c.q_full));
             unsigned long long path = 0;
-            const bool live = row < rows, warp_live = row0 + (warp & 3) * 32 < rows;
             if ((s.tile0 + s.n) * kN > ctx && live) {  // a tile with drafted slots
-                const int t = row / group + 1;
+                const int t = quotient(row, plan.by_group) + 1;
                 if (a.parent) {
                     for (int i = t; i > 0;) {
                         path |= 1ull << (i - 1);
@@ -453,11 +547,15 @@ attend(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtens
                                 if (!(seen >> i & 1)) x[k][i] = 0xff800000u;  // -inf
                         }
                     }
-                    float top = -INFINITY;
+                    float tops[8];  // eight chains: a single one would wait on itself
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) tops[i] = -INFINITY;
 #pragma unroll
                     for (int k = 0; k < kN / 32; ++k)
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) top = fmaxf(top, __uint_as_float(x[k][i]));
+                        for (int i = 0; i < 32; ++i) tops[i & 7] = fmaxf(tops[i & 7], __uint_as_float(x[k][i]));
+                    float top = fmaxf(fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])),
+                                      fmaxf(fmaxf(tops[4], tops[5]), fmaxf(tops[6], tops[7])));
                     if (j == 0) {
                         m = top;
                     } else {
@@ -483,7 +581,7 @@ attend(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtens
                     }
                     const float mc = m == -INFINITY ? 0.f : m * scale;  // nothing seen yet: every weight is 0
                     const float2 sc = make_float2(scale, scale), mn = make_float2(-mc, -mc);
-                    float2 part = make_float2(0.f, 0.f);
+                    float2 part[4] = {};
 #pragma unroll
                     for (int k = 0; k < kN / 64; ++k) {
                         unsigned p[32];
@@ -493,12 +591,12 @@ attend(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtens
                             float2 f = fma2(make_float2(__uint_as_float(y[0]), __uint_as_float(y[1])), sc, mn);
                             f.x = ex2(f.x);
                             f.y = ex2(f.y);
-                            part = add2(part, f);
+                            part[i & 3] = add2(part[i & 3], f);
                             p[i] = pack_bf16(f.x, f.y);
                         }
                         gdntc::tmem_st32(s_addr + k * 32, p);
                     }
-                    sum = add2(sum, part);
+                    sum = add2(sum, add2(add2(part[0], part[1]), add2(part[2], part[3])));
                     gdntc::tmem_wait_st();
                 }
                 if (edge && w == 0) {
@@ -544,10 +642,10 @@ attend(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtens
                 const bool whole = s.n == s.tiles;
                 const float total = sum.x + sum.y, inv = whole ? 1.f / total : 1.f;
                 const unsigned long long odd = *(volatile unsigned long long *)&c.odd_nodes[seg & 3] & path;
-                const size_t out_row = (((size_t)s.b * a.n_tok + row / group) * a.h_q + kv * group + row % group) * D;
                 const size_t piece = 2 * blockIdx.x + (first_segment ? 0 : 1);
                 const int pr = w * kM + row_in_tile;
                 const Buf bo{pieces.o, (size_t)2 * gridDim.x * W * kM * D * 4}, bms{pieces.ms, (size_t)2 * gridDim.x * W * kM * 8};
+                if (!whole && row_in_tile == 0 && w == 0) pieces.unit[piece] = s.b * plan.units + s.unit;
                 if (!whole && live) {
                     float2 *f = pieces.ms + piece * (W * kM) + pr;
                     if (GDN_IN(f, 8, bms, st)) *f = make_float2(m == -INFINITY ? m : m * scale, total);
@@ -581,7 +679,7 @@ attend(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtens
                         }
                     }
                     if (whole) {
-                        __nv_bfloat16 *to = static_cast<__nv_bfloat16 *>(a.out) + out_row + k;
+                        __nv_bfloat16 *to = static_cast<__nv_bfloat16 *>(a.out) + q_row + k;
 #pragma unroll
                         for (int i = 0; i < 32; i += 8)
                             if (GDN_IN(to + i, 16, bout, st))
@@ -602,93 +700,130 @@ attend(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtens
             ++seg;
         }
     }
+    // requests that are left out get zeros
+    for (int b = blockIdx.x; b < a.batch; b += gridDim.x)
+        if (gdnattn::slots_of(a, b) == 0) {
+            const size_t units16 = (size_t)a.n_tok * a.h_q * D / 8;
+            uint4 *to = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out)) + b * units16;
+            const Buf bout{a.out, (size_t)a.batch * units16 * 16};
+            for (size_t i = tid; i < units16; i += S::kThreads)
+                if (GDN_IN(to + i, 16, bout, st)) to[i] = make_uint4(0, 0, 0, 0);
+        }
     __syncthreads();
     if (c.quit && tid == 0 && st) atomicOr(st, GDN_DEV_SCHED);
-    if (warp == kMmaWarp) {
+    if (warp == kScoreWarp) {
         gdntc::fence_after_sync();
         gdntc::tmem_dealloc<kTmemCols>(tmem);
     }
 }
 
-// grid (B * units * row chunks, D / 32): 32 rows of one unit, 32 columns; the
-// eight warps take its pieces in turn and their sums meet in shared memory.
+// The shared units' pieces added up. An item is 32 rows x 8 columns of one
+// unit; a block's eight warps are 8 / `share` items of `share` warps, which take
+// the item's pieces in turn, eight at a time: a piece at a time would wait for
+// memory with each. There are at most min(units, blocks - 1) shared units: with
+// fewer units than blocks an item's unit is its index, otherwise it is the one
+// cut by the beginning of block `index`, if that is its first cut.
 template <int D, int W>
-__global__ void __launch_bounds__(256) join_pieces(const __grid_constant__ AttnArgs a, const __grid_constant__ Pieces pieces, int blocks) {
-    constexpr int kN = Shape<D, W>::kN, kRows = W * kM;
-    __shared__ float4 part[8][8][32];
+__global__ void __launch_bounds__(256)
+join_pieces(const __grid_constant__ AttnArgs a, const __grid_constant__ Plan plan, const __grid_constant__ Pieces pieces,
+            int share, int items, int chunks, bool by_unit) {
+    constexpr int kRows = W * kM, kCols = D / 8, kAhead = 8;
+    __shared__ float4 part[8][2][32];
     __shared__ float top[8][32], total[8][32];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, d4 = blockIdx.y * 8;
-    const int group = a.h_q / a.h_kv, rows = a.n_tok * group;
-    const int m_groups = (rows + kRows - 1) / kRows, units = a.h_kv * m_groups, chunks = (min(rows, kRows) + 31) / 32;
-    const int chunk = blockIdx.x % chunks, unit = blockIdx.x / chunks % units, b = blockIdx.x / chunks / units;
-    const int pr = chunk * 32 + lane, row = unit % m_groups * kRows + pr;
+    __shared__ unsigned short list[8][2 * kMaxBlocks];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int item = blockIdx.x * (8 / share) + warp / share, which = warp % share;
+    const int d4 = item % kCols * 2, chunk = item / kCols % chunks, index = item / kCols / chunks;
+    const int pr = chunk * 32 + lane;
     int32_t *st = a.status;
-    const Buf bo{pieces.o, (size_t)2 * blocks * kRows * D * 4}, bms{pieces.ms, (size_t)2 * blocks * kRows * 8},
+    const Buf bo{pieces.o, (size_t)2 * plan.blocks * kRows * D * 4}, bms{pieces.ms, (size_t)2 * plan.blocks * kRows * 8},
         bout{a.out, (size_t)a.batch * a.n_tok * a.h_q * D * 2};
     gdndev::pdl_wait();
-    const int slots = gdnattn::slots_of(a, b), tiles = (slots + kN - 1) / kN;
-    const bool live = row < rows;
-    __nv_bfloat16 *to = static_cast<__nv_bfloat16 *>(a.out) +
-                        (((size_t)b * a.n_tok + row / group) * a.h_q + unit / m_groups * group + row % group) * D + d4 * 4 + warp * 4;
-    if (tiles == 0) {  // left out
-        if (live && GDN_IN(to, 8, bout, st)) *reinterpret_cast<uint2 *>(to) = make_uint2(0, 0);
-        return;
+    // the unit's pieces, from the blocks' notes
+    int note[kNotes], unit = index;
+#pragma unroll
+    for (int i = 0; i < kNotes; ++i) {
+        const int p = i * 32 + lane;
+        note[i] = p < 2 * plan.blocks ? __ldcg(pieces.unit + p) : -1;
     }
-    const long long all = tiles_before<kN>(a, units, a.batch);
-    const long long first = tiles_before<kN>(a, units, b) + (long long)unit * tiles, last = first + tiles - 1;
-    const int c0 = (int)(((first + 1) * blocks - 1) / all), c1 = (int)(((last + 1) * blocks - 1) / all);
-    if (c0 == c1) return;  // one block had the whole unit and has written it
-    float m = -INFINITY, sum = 0.f;
-    float4 o[8];
+    if (!by_unit) unit = index < plan.blocks ? __ldcg(pieces.unit + 2 * index) : -1;
+    int n = 0;
+    if (unit >= 0) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int c = c0 + warp; c <= c1; c += 8) {
-        const long long start = range_start(all, c, blocks);
-        if (start == range_start(all, c + 1, blocks)) continue;  // no tiles
-        const size_t piece = 2 * c + (start < first ? 1 : 0);    // a block's first piece, or its last
-        const float2 *fm = pieces.ms + piece * kRows + pr;
-        const float4 *fo = pieces.o + (piece * (D / 4) + d4) * kRows + pr;
-        if (!live) continue;
-        const float2 ms = GDN_IN(fm, 8, bms, st) ? __ldcg(fm) : make_float2(-INFINITY, 0.f);
-        float4 x[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            x[i] = GDN_IN(fo + i * kRows, 16, bo, st) ? __ldcg(fo + i * kRows) : make_float4(0.f, 0.f, 0.f, 0.f);
-        if (ms.x == -INFINITY && ms.y == 0.f) continue;  // nothing there that the row sees
-        const float m2 = fmaxf(m, ms.x), wo = m == -INFINITY ? 0.f : ex2(m - m2), wn = ms.x == m2 ? 1.f : ex2(ms.x - m2);
-        m = m2;
-        sum = sum * wo + ms.y * wn;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            o[i].x = o[i].x * wo + x[i].x * wn;
-            o[i].y = o[i].y * wo + x[i].y * wn;
-            o[i].z = o[i].z * wo + x[i].z * wn;
-            o[i].w = o[i].w * wo + x[i].w * wn;
+        for (int i = 0; i < kNotes; ++i) {
+            const unsigned here = __ballot_sync(~0u, note[i] == unit);
+            if (note[i] == unit) list[warp][n + __popc(here & ((1u << lane) - 1))] = (unsigned short)(i * 32 + lane);
+            n += __popc(here);
         }
+    }
+    __syncwarp();
+    // below two pieces, one block had the whole unit and has written it
+    const bool mine = item < items && n >= 2 && (by_unit || list[warp][1] == 2 * index);
+    const int b = mine ? unit / plan.units : 0, in_request = unit - b * plan.units, kv = mine ? in_request / plan.m_groups : 0;
+    const int row = (in_request - kv * plan.m_groups) * kRows + pr;
+    const bool live = mine && row < plan.rows;
+    float m = -INFINITY, sum = 0.f;
+    float4 o[2] = {};
+    for (int k0 = live ? which : n; k0 < n; k0 += share * kAhead) {
+        float2 ms[kAhead];
+        float4 x[kAhead][2];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            ms[u] = make_float2(-INFINITY, 0.f);
+            x[u][0] = x[u][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (k0 + u * share < n) {
+                const size_t piece = list[warp][k0 + u * share];
+                const float2 *fm = pieces.ms + piece * kRows + pr;
+                const float4 *fo = pieces.o + (piece * (D / 4) + d4) * kRows + pr;
+                if (GDN_IN(fm, 8, bms, st)) ms[u] = __ldcg(fm);
+                if (GDN_IN(fo, 16, bo, st)) x[u][0] = __ldcg(fo);
+                if (GDN_IN(fo + kRows, 16, bo, st)) x[u][1] = __ldcg(fo + kRows);
+            }
+        }
+        float m2 = m;
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) m2 = fmaxf(m2, ms[u].x);
+        const float f0 = m == -INFINITY ? 0.f : ex2(m - m2);
+        sum *= f0;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) o[i] = make_float4(o[i].x * f0, o[i].y * f0, o[i].z * f0, o[i].w * f0);
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            if (ms[u].x == -INFINITY && ms[u].y == 0.f) continue;  // nothing there that the row sees
+            const float f = ms[u].x == m2 ? 1.f : ex2(ms[u].x - m2);
+            sum = fmaf(ms[u].y, f, sum);
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                o[i] = make_float4(fmaf(x[u][i].x, f, o[i].x), fmaf(x[u][i].y, f, o[i].y), fmaf(x[u][i].z, f, o[i].z),
+                                   fmaf(x[u][i].w, f, o[i].w));
+        }
+        m = m2;
     }
     top[warp][lane] = m;
     total[warp][lane] = sum;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) part[warp][i][lane] = o[i];
+    part[warp][0][lane] = o[0];
+    part[warp][1][lane] = o[1];
     __syncthreads();
-    // warp i joins the eight sums of column group i
-    float mm = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < 8; ++w) mm = fmaxf(mm, top[w][lane]);
-    float l = 0.f;
-    float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int w = 0; w < 8; ++w) {
+    if (!live || which != 0) return;
+    float mm = -INFINITY, l = 0.f;
+    for (int w = warp; w < warp + share; ++w) mm = fmaxf(mm, top[w][lane]);
+    o[0] = o[1] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int w = warp; w < warp + share; ++w) {
         const float tw = top[w][lane];
         if (tw == -INFINITY && total[w][lane] == 0.f) continue;
         const float f = tw == mm ? 1.f : ex2(tw - mm);
-        const float4 x = part[w][warp][lane];
-        l += total[w][lane] * f;
-        r.x += x.x * f, r.y += x.y * f, r.z += x.z * f, r.w += x.w * f;
+        l = fmaf(total[w][lane], f, l);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const float4 x = part[w][i][lane];
+            o[i] = make_float4(fmaf(x.x, f, o[i].x), fmaf(x.y, f, o[i].y), fmaf(x.z, f, o[i].z), fmaf(x.w, f, o[i].w));
+        }
     }
     const float inv = 1.f / l;
-    if (live && GDN_IN(to, 8, bout, st))
-        *reinterpret_cast<uint2 *>(to) = make_uint2(pack_bf16(r.x * inv, r.y * inv), pack_bf16(r.z * inv, r.w * inv));
+    __nv_bfloat16 *to = static_cast<__nv_bfloat16 *>(a.out) + row_offset(a, plan, b, kv, row) * D + d4 * 4;
+    if (GDN_IN(to, 16, bout, st))
+        *reinterpret_cast<uint4 *>(to) = make_uint4(pack_bf16(o[0].x * inv, o[0].y * inv), pack_bf16(o[0].z * inv, o[0].w * inv),
+                                                    pack_bf16(o[1].x * inv, o[1].y * inv), pack_bf16(o[1].z * inv, o[1].w * inv));
 }
 
 using Encode = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
@@ -722,7 +857,7 @@ bool pool_map(CUtensorMap *map, const attn_dims *d, const void *pool, int kn) {
 
 int block_count() {
     const int sms = gdnhost::sm_count();
-    return sms > 0 ? sms : 152;
+    return sms <= 0 ? 152 : sms < kMaxBlocks ? sms : kMaxBlocks;
 }
 
 int m_tiles(const attn_dims *d, int n_tok) {
@@ -743,14 +878,23 @@ int launch(const attn_dims *d, const AttnArgs &a, void *ws, cudaStream_t st) {
     CUtensorMap k_map, v_map;
     if (!pool_map(&k_map, d, a.k_pages, S::kN) || !pool_map(&v_map, d, a.v_pages, S::kN)) return GDN_ERR_CUDA;
     const int blocks = block_count();
-    const Pieces pieces{static_cast<float4 *>(ws),
-                        reinterpret_cast<float2 *>(static_cast<char *>(ws) + (size_t)2 * blocks * W * kM * D * 4)};
-    if (gdndev::launch_pdl(attend<D, W>, dim3(blocks), dim3(S::kThreads), S::kSmem, st, k_map, v_map, a, pieces) != cudaSuccess)
+    char *at = static_cast<char *>(ws);
+    const size_t rows_of_pieces = (size_t)2 * blocks * W * kM;
+    const Pieces pieces{reinterpret_cast<float4 *>(at), reinterpret_cast<float2 *>(at + rows_of_pieces * D * 4),
+                        reinterpret_cast<int *>(at + rows_of_pieces * (D * 4 + 8))};
+    const int group = a.h_q / a.h_kv, rows = a.n_tok * group, m_groups = (rows + W * kM - 1) / (W * kM);
+    auto by = [](int n) { return (unsigned)(((1ull << 32) + n - 1) / n); };
+    const Plan plan{group, rows, m_groups, a.h_kv * m_groups, blocks, by(group), by(m_groups), by(blocks)};
+    if (gdndev::launch_pdl(attend<D, W>, dim3(blocks), dim3(S::kThreads), S::kSmem, st, k_map, v_map, a, plan, pieces) != cudaSuccess)
         return GDN_ERR_CUDA;
-    const int rows = a.n_tok * (a.h_q / a.h_kv), in_unit = rows < W * kM ? rows : W * kM;
-    const int64_t units = (int64_t)a.batch * a.h_kv * ((rows + W * kM - 1) / (W * kM));
-    return gdndev::launch_pdl(join_pieces<D, W>, dim3((unsigned)(units * ((in_unit + 31) / 32)), D / 32), dim3(256), 0, st, a,
-                              pieces, blocks) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+    // a unit has about blocks / units pieces, and one more
+    const int64_t units = (int64_t)a.batch * plan.units;
+    const bool by_unit = units < blocks;
+    const int indexes = by_unit ? (int)units : blocks, per_unit = blocks / indexes + 1;
+    const int share = per_unit <= 8 ? 1 : per_unit <= 16 ? 2 : 8;
+    const int chunks = ((rows < W * kM ? rows : W * kM) + 31) / 32, items = indexes * chunks * (D / 8);
+    return gdndev::launch_pdl(join_pieces<D, W>, dim3((items * share + 7) / 8), dim3(256), 0, st, a, plan, pieces, share, items,
+                              chunks, by_unit) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
 }  // namespace
@@ -758,7 +902,7 @@ int launch(const attn_dims *d, const AttnArgs &a, void *ws, cudaStream_t st) {
 namespace gdnattn {
 
 size_t tc_workspace(const attn_dims *d, int n_tok) {
-    return (size_t)2 * block_count() * m_tiles(d, n_tok) * kM * (d->d_head * 4 + 8);
+    return (size_t)2 * block_count() * (m_tiles(d, n_tok) * kM * (d->d_head * 4 + 8) + 4);
 }
 
 int tc_launch(const attn_dims *d, const AttnArgs &a, void *ws, cudaStream_t st) {
