@@ -718,21 +718,24 @@ attend(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtens
 }
 
 // The shared units' pieces added up. An item is 32 rows x 8 columns of one
-// unit; a block's eight warps are 8 / `share` items of `share` warps, which take
-// the item's pieces in turn, eight at a time: a piece at a time would wait for
-// memory with each. There are at most min(units, blocks - 1) shared units: with
-// fewer units than blocks an item's unit is its index, otherwise it is the one
-// cut by the beginning of block `index`, if that is its first cut.
+// unit; a block's four warps are 4 / `share` items of `share` warps, which take
+// the item's pieces in turn, four at a time: a piece at a time would wait for
+// memory with each. Small blocks of few registers: all of them fit the GPU at
+// once. There are at most min(units, blocks - 1) shared units: with fewer units
+// than blocks an item's unit is its index, otherwise it is the one cut by the
+// beginning of block `index`, if that is its first cut.
+constexpr int kJoinWarps = 4;
+
 template <int D, int W>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(kJoinWarps * 32, 8)
 join_pieces(const __grid_constant__ AttnArgs a, const __grid_constant__ Plan plan, const __grid_constant__ Pieces pieces,
             int share, int items, int chunks, bool by_unit) {
-    constexpr int kRows = W * kM, kCols = D / 8, kAhead = 8;
-    __shared__ float4 part[8][2][32];
-    __shared__ float top[8][32], total[8][32];
-    __shared__ unsigned short list[8][2 * kMaxBlocks];
+    constexpr int kRows = W * kM, kCols = D / 8, kAhead = 4;
+    __shared__ float4 part[kJoinWarps][2][32];
+    __shared__ float top[kJoinWarps][32], total[kJoinWarps][32];
+    __shared__ unsigned short list[kJoinWarps][2 * kMaxBlocks];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int item = blockIdx.x * (8 / share) + warp / share, which = warp % share;
+    const int item = (blockIdx.x * kJoinWarps + warp) / share, which = warp % share;
     const int d4 = item % kCols * 2, chunk = item / kCols % chunks, index = item / kCols / chunks;
     const int pr = chunk * 32 + lane;
     int32_t *st = a.status;
@@ -746,6 +749,7 @@ join_pieces(const __grid_constant__ AttnArgs a, const __grid_constant__ Plan pla
         const int p = i * 32 + lane;
         note[i] = p < 2 * plan.blocks ? __ldcg(pieces.unit + p) : -1;
     }
+    // (the unit's number beside the notes, not after them)
     if (!by_unit) unit = index < plan.blocks ? __ldcg(pieces.unit + 2 * index) : -1;
     int n = 0;
     if (unit >= 0) {
@@ -891,9 +895,9 @@ int launch(const attn_dims *d, const AttnArgs &a, void *ws, cudaStream_t st) {
     const int64_t units = (int64_t)a.batch * plan.units;
     const bool by_unit = units < blocks;
     const int indexes = by_unit ? (int)units : blocks, per_unit = blocks / indexes + 1;
-    const int share = per_unit <= 8 ? 1 : per_unit <= 16 ? 2 : 8;
+    const int share = per_unit <= 4 ? 1 : per_unit <= 8 ? 2 : 4;
     const int chunks = ((rows < W * kM ? rows : W * kM) + 31) / 32, items = indexes * chunks * (D / 8);
-    return gdndev::launch_pdl(join_pieces<D, W>, dim3((items * share + 7) / 8), dim3(256), 0, st, a, plan, pieces, share, items,
+    return gdndev::launch_pdl(join_pieces<D, W>, dim3((items * share + kJoinWarps - 1) / kJoinWarps), dim3(kJoinWarps * 32), 0, st, a, plan, pieces, share, items,
                               chunks, by_unit) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
