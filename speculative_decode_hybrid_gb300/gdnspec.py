@@ -102,6 +102,8 @@ _lib = None
 def load(path: Optional[str] = None):
     """Load libgdnspec.so (built by speculative_decode_hybrid_gb300.build)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -169,19 +171,36 @@ def _ptr(t) -> Optional[int]:
     """Raw pointer of a tensor / numpy array / int / None."""
     if t is None:
         return None
+    try:
+        return t.data_ptr()
+    except AttributeError:
+        pass
     if isinstance(t, int):
         return t
-    if hasattr(t, "data_ptr"):
-        return t.data_ptr()
     if hasattr(t, "ctypes"):
         return t.ctypes.data
     raise TypeError(f"cannot take a pointer of {type(t)}")
 
 
+_raw_stream = None
+
+
+def _current_stream() -> int:
+    """Handle of the current stream, without the Stream object that
+    torch.cuda.current_stream() builds (3 us, a third of a small call) where
+    this PyTorch has the getter its own compiled code uses."""
+    global _raw_stream
+    import torch
+    if _raw_stream is None:
+        raw, dev = getattr(torch._C, "_cuda_getCurrentRawStream", None), getattr(torch._C, "_cuda_getDevice", None)
+        torch.cuda.init()
+        _raw_stream = (lambda: raw(dev())) if raw and dev else (lambda: torch.cuda.current_stream().cuda_stream)
+    return _raw_stream()
+
+
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
