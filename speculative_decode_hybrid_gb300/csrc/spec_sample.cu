@@ -46,15 +46,14 @@ constexpr int kThreads = 256;
 constexpr int kBlocksPerSm = 6;
 constexpr int kPickThreads = 512;
 constexpr int kCluster = 8;
-constexpr int kAhead = 5;           // 16-byte loads of each row a thread of sample_pick has in flight
+constexpr int kAhead = 3;           // 16-byte loads of each row a thread of sample_pick has in flight
 constexpr int kMaxPieces = 40;      // blocks that a row may be spread over
 static_assert(kMaxPieces <= 64, "two pieces a lane");
 constexpr int kMinPart = 1024;      // values a block takes at least
 constexpr int kMaxNodes = GDN_MAX_TOKENS + 1;
 constexpr float kLog2e = 1.4426950408889634f;
 
-// A row's maximum and the sum of exp((x - max) / T) (T == 0: the number of
-// values equal to the maximum).
+// A row's maximum and the sum of exp((x - max) / T).
 struct Stat {
     float m, s;
 };
@@ -65,15 +64,14 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
-// exp((x - m) / T); c = log2(e) / T, or 0 for T == 0. The difference is taken
-// first: near the maximum, where the weight lies, it is exact.
-__device__ __forceinline__ float weight(float x, float m, float c) {
-    return c > 0.f ? ex2((x - m) * c) : (x == m ? 1.f : (x == x ? 0.f : x));
-}
+// exp((x - m) / T), c = log2(e) / T. The difference is taken first: near the
+// maximum, where the weight lies, it is exact.
+__device__ __forceinline__ float weight(float x, float m, float c) { return ex2((x - m) * c); }
 
+// T == 0 is the limit: a factor that leaves weight only where x - m is 0.
 __device__ __forceinline__ float coefficient(const float *temperature, int b) {
     const float t = temperature ? temperature[b] : 1.f;
-    return t > 0.f ? kLog2e / t : 0.f;
+    return t > 0.f ? fminf(kLog2e / t, 3e38f) : 3e38f;
 }
 
 // Join two parts' statistics. A part without a value above -inf has m = -inf
@@ -96,13 +94,8 @@ __device__ __forceinline__ void absorb(Stat &st, const float (&x)[K], float c) {
     }
     const float m = st.m == -INFINITY ? 0.f : st.m;  // all -inf so far: every weight is exp(-inf) = 0
     float s[4] = {};
-    if (c > 0.f) {
 #pragma unroll
-        for (int i = 0; i < K; ++i) s[i & 3] += ex2((x[i] - m) * c);
-    } else {
-#pragma unroll
-        for (int i = 0; i < K; ++i) s[i & 3] += weight(x[i], m, c);
-    }
+    for (int i = 0; i < K; ++i) s[i & 3] += weight(x[i], m, c);
     st.s += (s[0] + s[1]) + (s[2] + s[3]);
 }
 
@@ -114,7 +107,7 @@ struct Deal {
 
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
 sample_rows(int n_nodes, int vocab, Deal deal, const float *__restrict__ logits, const float *__restrict__ temperature,
-            Stat *__restrict__ stats, int rows, int32_t *dev_status) {
+            const float *__restrict__ noise, Stat *__restrict__ stats, int rows, int32_t *dev_status) {
     __shared__ Stat warp_stat[2][kThreads / 32];
     const int tid = threadIdx.x;
     const Buf bl{logits, (size_t)deal.total * 4}, bs{stats, (size_t)rows * kMaxPieces * sizeof(Stat)};
@@ -171,6 +164,9 @@ sample_rows(int n_nodes, int vocab, Deal deal, const float *__restrict__ logits,
         }
         at = end;
     }
+    // the noise that sample_pick reads, on its way to L2
+    const size_t lines = (size_t)(rows / n_nodes) * vocab * 4;
+    gdndev::prefetch_l2_range(noise, lines, blockIdx.x * kThreads + tid, gridDim.x * kThreads);
 }
 
 struct PickArgs {
@@ -208,7 +204,7 @@ __device__ __forceinline__ T cluster_reduce(T v, T *warp_buf, T *cta_buf, Op op)
     return v;
 }
 
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPickThreads)
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPickThreads, 2)
 sample_pick(PickArgs a) {
     namespace cg = cooperative_groups;
     __shared__ float row_m[kMaxNodes], row_s[kMaxNodes];
@@ -362,7 +358,7 @@ sample_pick(PickArgs a) {
     // the next token: the largest rest / noise of the accepted row
     const float m = row_m[node], total = row_s[node], inv = 1.f / total;
     const bool defined = total == total;
-    if (!a.draft && tid > node && tid < N && parent_of[tid] == node && token_of[tid] >= 0)
+    if (!a.draft && tid > node && tid < N && parent_of[tid] == node && token_of[tid] >= 0 && !gone_before[tid])
         removed[atomicAdd(&n_removed, 1)] = token_of[tid];  // in any order: only looked up
     __syncthreads();
     const int gone_tokens = n_removed;
@@ -375,17 +371,33 @@ sample_pick(PickArgs a) {
     // this thread's best; with_q: of (p - coef q)+ / noise, else of p / noise less
     // the removed tokens (without p's divisor, which is the same for all)
     auto scan = [&](auto with_q, int gone) {
+        // the removed tokens among this thread's values: two are compared with
+        // everywhere, more (a token is seldom removed at all) looked up
+        int gone0 = -1, gone1 = -1;
+        bool many = false;
+        for (int j = 0; j < gone; ++j) {
+            const int r = removed[j], i = r - lo;
+            if (i < 0 || i >= hi - lo || (wide ? i / 4 : i) % kPickThreads != tid) continue;
+            many |= gone1 >= 0;
+            gone1 = gone0;
+            gone0 = r;
+        }
         const float *q = with_q ? a.draft + ((size_t)b * (N - 1) + node) * V : nullptr;
         top = 0.f, at = 0, top_x = 0.f;
         auto offer = [&](int v, float x, float e, float qv) {
             float w = weight(x, m, c);
             if constexpr (with_q) w = fmaf(-coef, qv, w * inv);
-            const float f = w > 0.f ? __fdividef(w, e) : 0.f;
-            if (f > top) {
-                bool out = false;
-                for (int j = 0; j < gone; ++j) out |= removed[j] == v;
-                if (!out) top = f, at = v, top_x = x;
+            if constexpr (!with_q) {
+                if (v == gone0 || v == gone1) w = 0.f;
+                if (many)
+                    for (int j = 0; j < gone; ++j)
+                        if (removed[j] == v) w = 0.f;
             }
+            const float f = __fdividef(w, e);
+            const bool more = f > top && w > 0.f;  // selected, not branched over: some lane of a warp nearly always has more
+            top = more ? f : top;
+            at = more ? v : at;
+            top_x = more ? x : top_x;
         };
         if (wide) {
             for (int v0 = lo + tid * 4; v0 < hi; v0 += kPickThreads * 4 * kAhead) {
@@ -501,7 +513,7 @@ extern "C" int spec_accept_sample(int32_t batch, int32_t n_nodes, int32_t vocab,
     Stat *stats = static_cast<Stat *>(workspace);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (gdndev::launch_pdl(sample_rows, dim3(deal.blocks), dim3(kThreads), 0, st, n_nodes, vocab, deal, logits, temperature,
-                           stats, rows, dev_status) != cudaSuccess)
+                           noise, stats, rows, dev_status) != cudaSuccess)
         return GDN_ERR_CUDA;
     PickArgs a{n_nodes, vocab, deal, logits, draft_probs, tokens, parent_dev, temperature, uniforms, noise,
                accept_len, accept_node, next_token, token_prob, stats, dev_status};
