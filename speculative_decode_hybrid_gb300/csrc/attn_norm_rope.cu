@@ -3,18 +3,22 @@
 // projected rows (the hybrid's attention layers of lucebox PR #506, Summary;
 // openinfer PR #626, What Changed).
 //
-// A head of D values is D / 8 lanes with 8 consecutive values each (16 bytes
-// of bf16, twice 16 of f32). The sum of squares is a butterfly over the head's
-// lanes; the partner of a value under the rotation lies rot_dim / 2 values on,
-// which is a fixed number of lanes (rot_dim is a multiple of 16), so the
-// rotation is eight shuffles; with GDN_ROPE_PAIRS it is the neighbour in the
-// same lane. Every input is read once, every output written once, and a
-// token's cosines and sines are held in registers over its heads: the kernel is
-// bound by the bytes of qkv, q and the cache rows.
+// A head of D values is D / 8 lanes of two runs of four values: under the
+// rotation the second run is the first's partner, rot_dim / 2 values on, so that
+// a pair never leaves its lane (with GDN_ROPE_PAIRS the runs are neighbours and
+// the pairs within them); the sum of squares is a butterfly over the head's
+// lanes. A warp takes a token's heads in turn, 32 / (D / 8) at a time, the
+// queries, the keys and the values each in a loop of its own, with the token's
+// cosines and sines and the norm weights in registers: what is done per head is
+// its loads, its arithmetic (two values an instruction) and its stores. A first
+// form that chose between the three kinds head by head took 210 instructions a
+// step and was bound by them (56 us for 8,002 tokens of 48 heads of 128);
+// this one is bound by the bytes of qkv, q and the cache rows.
 #include <cuda_runtime.h>
 
 #include <cmath>
 #include <initializer_list>
+#include <type_traits>
 
 #include "gdn_device.cuh"
 #include "gdn_host.h"
@@ -23,11 +27,15 @@
 namespace {
 
 using gdndev::Buf;
+using gdndev::fma2;
+using gdndev::mul2;
 
 constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kBlocksPerSm = 4;
 
 struct RopeArgs {
-    int n_tok, h_q, h_kv, page_shift, n_pages, width, rot, max_pos, tokens_per_block;
+    int n_tok, h_q, h_kv, page_shift, n_pages, width, rot, max_pos, warps_per_token;
     int64_t tokens, stride;
     const void *qkv, *q_norm, *k_norm;
     float eps, offset;
@@ -39,166 +47,207 @@ struct RopeArgs {
     bool pairs;
 };
 
+// Four values as they are stored.
 template <bool BF16>
-__device__ __forceinline__ void load8(const void *p, size_t i, float (&x)[8]) {
+struct Run {
+    unsigned u[BF16 ? 2 : 4];
+};
+
+template <bool BF16>
+__device__ __forceinline__ Run<BF16> load_run(const char *p) {
+    Run<BF16> r;
     if constexpr (BF16) {
-        const uint4 u = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p) + i);
-        const unsigned w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            x[2 * j] = __uint_as_float(w[j] << 16);
-            x[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
-        }
+        const uint2 v = *reinterpret_cast<const uint2 *>(p);
+        r.u[0] = v.x, r.u[1] = v.y;
     } else {
-        const float4 *f = reinterpret_cast<const float4 *>(static_cast<const float *>(p) + i);
-        const float4 a = f[0], b = f[1];
-        x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+        const uint4 v = *reinterpret_cast<const uint4 *>(p);
+        r.u[0] = v.x, r.u[1] = v.y, r.u[2] = v.z, r.u[3] = v.w;
     }
+    return r;
 }
 
 template <bool BF16>
-__device__ __forceinline__ void store8(void *p, size_t i, const float (&x)[8]) {
-    if constexpr (BF16) {
-        unsigned w[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * j], x[2 * j + 1]);
-            w[j] = *reinterpret_cast<const unsigned *>(&h);
-        }
-        *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p) + i) = make_uint4(w[0], w[1], w[2], w[3]);
-    } else {
-        float4 *f = reinterpret_cast<float4 *>(static_cast<float *>(p) + i);
-        f[0] = make_float4(x[0], x[1], x[2], x[3]);
-        f[1] = make_float4(x[4], x[5], x[6], x[7]);
-    }
+__device__ __forceinline__ void store_run(char *p, const Run<BF16> &r) {
+    if constexpr (BF16)
+        *reinterpret_cast<uint2 *>(p) = make_uint2(r.u[0], r.u[1]);
+    else
+        *reinterpret_cast<uint4 *>(p) = make_uint4(r.u[0], r.u[1], r.u[2], r.u[3]);
 }
 
-// grid (token blocks, head parts). A block's lane groups are dealt out to
-// tokens_per_block tokens; a token's groups take its heads in turn.
-template <bool BF16, int D>
-__global__ void __launch_bounds__(kThreads) qk_norm_rope(RopeArgs a) {
-    constexpr int kLanes = D / 8, kGroups = kThreads / kLanes, kElem = BF16 ? 2 : 4;
-    const int lane = threadIdx.x % kLanes, group = threadIdx.x / kLanes;
-    const int per_token = kGroups / a.tokens_per_block;
-    const int64_t token = (int64_t)blockIdx.x * a.tokens_per_block + group / per_token;
-    const bool live_token = token < a.tokens;
+template <bool BF16>
+__device__ __forceinline__ void widen(const Run<BF16> &r, float2 (&x)[2]) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+        x[j] = BF16 ? make_float2(__uint_as_float(r.u[j] << 16), __uint_as_float(r.u[j] & 0xffff0000u))
+                    : make_float2(__uint_as_float(r.u[BF16 ? 0 : 2 * j]), __uint_as_float(r.u[BF16 ? 0 : 2 * j + 1]));
+}
+
+template <bool BF16>
+__device__ __forceinline__ Run<BF16> narrow(const float2 (&x)[2]) {
+    Run<BF16> r;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        if constexpr (BF16) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(x[j].x, x[j].y);
+            r.u[j] = *reinterpret_cast<const unsigned *>(&h);
+        } else {
+            r.u[2 * j] = __float_as_uint(x[j].x), r.u[2 * j + 1] = __float_as_uint(x[j].y);
+        }
+    }
+    return r;
+}
+
+// grid (token blocks, parts): a block's eight warps are 8 / warps_per_token
+// tokens; with several parts a token's warps are spread over as many blocks.
+template <bool BF16, int D, bool PAIRS>
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm) qk_norm_rope(RopeArgs a) {
+    constexpr int kLanes = D / 8, kGroups = 32 / kLanes, kElem = BF16 ? 2 : 4, kRun = 4 * kElem, kHead = D * kElem;
+    constexpr int kAhead = BF16 ? 4 : 2;  // steps whose loads are in flight together
+    const int lane = threadIdx.x % kLanes, group = threadIdx.x % 32 / kLanes, warp = threadIdx.x / 32;
+    const int64_t token = (int64_t)blockIdx.x * (kWarps / a.warps_per_token) + warp / a.warps_per_token;
+    const int warps = a.warps_per_token * gridDim.y, mine = warp % a.warps_per_token + a.warps_per_token * blockIdx.y;
     int32_t *st = a.status;
-    const size_t B = a.batch, pool_bytes = ((size_t)a.n_pages * a.h_kv << a.page_shift) * D * kElem;
+    const size_t B = a.batch, pool_bytes = ((size_t)a.n_pages * a.h_kv << a.page_shift) * kHead;
     const Buf bx{a.qkv, ((size_t)(a.tokens - 1) * a.stride + (size_t)(a.h_q + 2 * a.h_kv) * D) * kElem},
-        bq{a.q_out, (size_t)a.tokens * a.h_q * D * kElem}, bk{a.k_pages, pool_bytes}, bv{a.v_pages, pool_bytes},
+        bq{a.q_out, (size_t)a.tokens * a.h_q * kHead}, bk{a.k_pages, pool_bytes}, bv{a.v_pages, pool_bytes},
         bpar{a.parent, B * (a.n_tok + 1) * 4}, btab{a.table, B * (size_t)a.width * 4},
         brope{a.rope, (size_t)a.max_pos * a.rot * 4};
+    // this lane's two runs of a head, in bytes, and whether they turn
+    const int half = a.rot / 2;
+    const bool turned = PAIRS ? lane * 8 < a.rot : lane * 4 < half;
+    const int d0 = (turned && !PAIRS ? lane * 4 : lane * 8) * kElem, d1 = (turned && !PAIRS ? half + lane * 4 : lane * 8 + 4) * kElem;
     gdndev::pdl_wait();
-    if (!live_token) return;  // whole lane groups: no shuffle below crosses one
-    const int b = (int)(token / a.n_tok), t = (int)(token % a.n_tok) + 1;
+    if (token >= a.tokens) return;
+    const int b = (int)((unsigned)token / (unsigned)a.n_tok), t = (int)token - b * a.n_tok + 1;
     const int ctx = a.ctx[b];
     int depth = t;
     if (a.parent) {
         depth = 0;
         const int32_t *row = a.parent + (size_t)b * (a.n_tok + 1);
         for (int i = t; i > 0; ++depth) {
-            int p = GDN_IN(row + i, 4, bpar, st) ? row[i] : i - 1;
-            if (p < 0 || p >= i) {
-                p = i - 1;
-                if (lane == 0 && st) atomicOr(st, GDN_DEV_TREE);
+            int up = GDN_IN(row + i, 4, bpar, st) ? row[i] : i - 1;
+            if (up < 0 || up >= i) {
+                up = i - 1;
+                if (threadIdx.x % 32 == 0 && st) atomicOr(st, GDN_DEV_TREE);
             }
-            i = p;
+            i = up;
         }
     }
     // a chain's last position bounds a tree's; a request is left out as a whole
-    const bool fits = ctx >= 0 && (int64_t)ctx + a.n_tok <= (int64_t)a.width << a.page_shift &&
-                      (a.rot == 0 || (int64_t)ctx + a.n_tok <= a.max_pos);
-    if (!fits) {
-        if (lane == 0 && st) atomicOr(st, GDN_DEV_LENGTH);
+    if (ctx < 0 || (int64_t)ctx + a.n_tok > (int64_t)a.width << a.page_shift ||
+        (a.rot > 0 && (int64_t)ctx + a.n_tok > a.max_pos)) {
+        if (threadIdx.x % 32 == 0 && st) atomicOr(st, GDN_DEV_LENGTH);
         return;
     }
     const int pos = ctx + depth - 1, slot = ctx + t - 1;
     const int32_t *entry = a.table + (size_t)b * a.width + (slot >> a.page_shift);
     const int page = GDN_IN(entry, 4, btab, st) ? *entry : -1;
     const bool page_ok = page >= 0 && page < a.n_pages;
-    if (!page_ok && lane == 0 && st) atomicOr(st, GDN_DEV_PAGE);
-
-    const int half = a.rot / 2, d0 = lane * 8;
-    // this lane's cosines and sines: of its values' pair indices
-    float cs[8], sn[8];
-    const bool turned = d0 < a.rot;
-    if (turned && a.pairs) {
-        const float *row = a.rope + (size_t)pos * a.rot + d0 / 2;
+    float2 cs[2] = {make_float2(1.f, 1.f), make_float2(1.f, 1.f)}, sn[2] = {};  // no turn: cosine 1, sine 0
+    if (turned) {
+        const float *row = a.rope + (size_t)pos * a.rot + lane * 4;
         if (GDN_IN(row, 16, brope, st) && GDN_IN(row + half, 16, brope, st)) {
             const float4 c = gdndev::ld4(row), s = gdndev::ld4(row + half);
-            cs[0] = cs[1] = c.x, cs[2] = cs[3] = c.y, cs[4] = cs[5] = c.z, cs[6] = cs[7] = c.w;
-            sn[0] = sn[1] = s.x, sn[2] = sn[3] = s.y, sn[4] = sn[5] = s.z, sn[6] = sn[7] = s.w;
+            cs[0] = make_float2(c.x, c.y), cs[1] = make_float2(c.z, c.w);
+            sn[0] = make_float2(s.x, s.y), sn[1] = make_float2(s.z, s.w);
         }
-    } else if (turned) {
-        const float *row = a.rope + (size_t)pos * a.rot + (d0 < half ? d0 : d0 - half);
-        if (GDN_IN(row, 32, brope, st)) load8<false>(row, 0, cs);
-        if (GDN_IN(row + half, 32, brope, st)) load8<false>(row + half, 0, sn);
     }
-    float wq[8], wk[8];
-    load8<BF16>(a.q_norm, d0, wq);
-    load8<BF16>(a.k_norm, d0, wk);
-    const int heads = a.h_q + 2 * a.h_kv, stride = per_token * gridDim.y;
-    const unsigned mask = kLanes == 32 ? ~0u : ((1u << kLanes) - 1) << (threadIdx.x % 32 / kLanes * kLanes);
-    for (int h = group % per_token + per_token * blockIdx.y; h < heads; h += stride) {
-        const size_t from = (size_t)token * a.stride + (size_t)h * D + d0;
-        float x[8] = {};
-        if (GDN_IN(static_cast<const char *>(a.qkv) + from * kElem, 8 * kElem, bx, st)) load8<BF16>(a.qkv, from, x);
-        if (h < a.h_q + a.h_kv) {
-            float s = 0.f;
+    if (!page_ok && threadIdx.x % 32 == 0 && st) atomicOr(st, GDN_DEV_PAGE);
+    const char *src = static_cast<const char *>(a.qkv) + token * a.stride * kElem;
+    const size_t page_at = ((((size_t)(page_ok ? page : 0) * a.h_kv) << a.page_shift) + (slot & ((1 << a.page_shift) - 1))) * kHead;
+    const int kv_step = kHead << a.page_shift;  // from a page's head to its next
+
+    // heads `first`, first + warps * kGroups, ... of one kind; from: its first
+    // head in the row; to, to_step: its first head's place and the way to the next
+    auto kind = [&](auto norm, int first_step, int count, const char *from, char *to, int to_step, const void *weights, Buf bto) {
+        float2 w[4];
+        if constexpr (norm) {
+            if (first_step * kGroups >= count) return;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) s = fmaf(x[j], x[j], s);
-#pragma unroll
-            for (int o = kLanes / 2; o; o >>= 1) s += __shfl_xor_sync(mask, s, o);
-            const float r = rsqrtf(s * (1.0f / D) + a.eps);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] *= r * ((h < a.h_q ? wq[j] : wk[j]) + a.offset);
-            if (a.pairs) {
-                if (turned) {
-#pragma unroll
-                    for (int j = 0; j < 8; j += 2) {
-                        const float u = x[j], v = x[j + 1];
-                        x[j] = u * cs[j] - v * sn[j];
-                        x[j + 1] = v * cs[j] + u * sn[j];
-                    }
-                }
-            } else if (a.rot > 0) {
-                // the partner lane: rot / 2 values away
-                const int hop = half / 8, src = turned ? (d0 < half ? lane + hop : lane - hop) : lane;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float y = __shfl_sync(mask, x[j], src, kLanes);
-                    if (turned) x[j] = d0 < half ? x[j] * cs[j] - y * sn[j] : x[j] * cs[j] + y * sn[j];
-                }
+            for (int j = 0; j < 2; ++j) {
+                float2 x[2];
+                widen<BF16>(load_run<BF16>(static_cast<const char *>(weights) + (j ? d1 : d0)), x);
+                w[2 * j] = make_float2(x[0].x + a.offset, x[0].y + a.offset);
+                w[2 * j + 1] = make_float2(x[1].x + a.offset, x[1].y + a.offset);
             }
         }
-        if (h < a.h_q) {
-            const size_t to = ((size_t)token * a.h_q + h) * D + d0;
-            if (GDN_IN(static_cast<char *>(a.q_out) + to * kElem, 8 * kElem, bq, st)) store8<BF16>(a.q_out, to, x);
-        } else if (page_ok) {
-            const int kv = h < a.h_q + a.h_kv ? h - a.h_q : h - a.h_q - a.h_kv;
-            void *pool = h < a.h_q + a.h_kv ? a.k_pages : a.v_pages;
-            const size_t to = ((((size_t)page * a.h_kv + kv) << a.page_shift) + (slot & ((1 << a.page_shift) - 1))) * D + d0;
-            if (GDN_IN(static_cast<char *>(pool) + to * kElem, 8 * kElem, (h < a.h_q + a.h_kv ? bk : bv), st))
-                store8<BF16>(pool, to, x);
+        for (int h0 = first_step * kGroups + group; h0 - group < count; h0 += kAhead * warps * kGroups) {
+            Run<BF16> raw[kAhead][2];
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                const int h = h0 + k * warps * kGroups;
+                const char *p = from + h * kHead;
+                if (h < count && GDN_IN(p + d0, kRun, bx, st) && GDN_IN(p + d1, kRun, bx, st))
+                    raw[k][0] = load_run<BF16>(p + d0), raw[k][1] = load_run<BF16>(p + d1);
+            }
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                const int h = h0 + k * warps * kGroups;
+                if (h - group >= count) break;  // the whole warp; a group past the end goes along
+                Run<BF16> out[2] = {raw[k][0], raw[k][1]};
+                if constexpr (norm) {
+                    float2 x[2], y[2];
+                    widen<BF16>(raw[k][0], x);
+                    widen<BF16>(raw[k][1], y);
+                    float2 s2 = mul2(x[0], x[0]);
+                    s2 = fma2(x[1], x[1], s2);
+                    s2 = fma2(y[0], y[0], s2);
+                    s2 = fma2(y[1], y[1], s2);
+                    float s = s2.x + s2.y;
+#pragma unroll
+                    for (int o = kLanes / 2; o; o >>= 1) s += __shfl_xor_sync(~0u, s, o);
+                    const float r = rsqrtf(fmaf(s, 1.0f / D, a.eps));
+                    const float2 rr = make_float2(r, r);
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) x[j] = mul2(mul2(x[j], rr), w[j]), y[j] = mul2(mul2(y[j], rr), w[2 + j]);
+                    if constexpr (PAIRS) {
+                        const float c4[4] = {cs[0].x, cs[0].y, cs[1].x, cs[1].y}, s4[4] = {sn[0].x, sn[0].y, sn[1].x, sn[1].y};
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            float2 &z = j < 2 ? x[j] : y[j - 2];
+                            z = make_float2(z.x * c4[j] - z.y * s4[j], z.y * c4[j] + z.x * s4[j]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            const float2 u = x[j], v = y[j], minus = make_float2(-sn[j].x, -sn[j].y);
+                            x[j] = fma2(v, minus, mul2(u, cs[j]));
+                            y[j] = fma2(u, sn[j], mul2(v, cs[j]));
+                        }
+                    }
+                    out[0] = narrow<BF16>(x);
+                    out[1] = narrow<BF16>(y);
+                }
+                char *p = to + (size_t)h * to_step;
+                if (h < count && GDN_IN(p + d0, kRun, bto, st) && GDN_IN(p + d1, kRun, bto, st))
+                    store_run<BF16>(p + d0, out[0]), store_run<BF16>(p + d1, out[1]);
+            }
         }
-    }
+    };
+    // the kinds' steps in one row, dealt out to the token's warps in turn
+    const int q_steps = (a.h_q + kGroups - 1) / kGroups, kv_steps = (a.h_kv + kGroups - 1) / kGroups;
+    auto start = [&](int steps_before) { return (mine + warps - steps_before % warps) % warps; };
+    kind(std::true_type{}, mine, a.h_q, src, static_cast<char *>(a.q_out) + token * a.h_q * kHead, kHead, a.q_norm, bq);
+    if (!page_ok) return;
+    kind(std::true_type{}, start(q_steps), a.h_kv, src + a.h_q * kHead, static_cast<char *>(a.k_pages) + page_at, kv_step, a.k_norm, bk);
+    kind(std::false_type{}, start(q_steps + kv_steps), a.h_kv, src + (a.h_q + a.h_kv) * kHead, static_cast<char *>(a.v_pages) + page_at,
+         kv_step, nullptr, bv);
 }
 
 template <bool BF16, int D>
 int launch(RopeArgs a, cudaStream_t st) {
-    constexpr int kGroups = kThreads / (D / 8);
-    const int heads = a.h_q + 2 * a.h_kv;
-    // few heads: several tokens share a block; few tokens: several blocks share
-    // a token's heads, until every lane group has one head
-    a.tokens_per_block = 1;
-    while (a.tokens_per_block * 2 <= kGroups && heads * a.tokens_per_block * 2 <= kGroups) a.tokens_per_block *= 2;
-    const int64_t blocks = (a.tokens + a.tokens_per_block - 1) / a.tokens_per_block;
-    const int sms = gdnhost::sm_count();
-    int parts = (heads * a.tokens_per_block + kGroups - 1) / kGroups;
-    const int64_t want = (2 * (sms > 0 ? sms : 152) + blocks - 1) / blocks;
-    if (parts > want) parts = (int)want;
-    return gdndev::launch_pdl(qk_norm_rope<BF16, D>, dim3((unsigned)blocks, parts < 1 ? 1 : parts), dim3(kThreads), 0, st,
-                              a) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+    constexpr int kGroups = 32 / (D / 8);
+    // many tokens: a warp each, as long as that fills the GPU; few: up to a warp
+    // for every step
+    const int sms = gdnhost::sm_count(), resident = kBlocksPerSm * kWarps * (sms > 0 ? sms : 152);
+    const int steps = (a.h_q + kGroups - 1) / kGroups + 2 * ((a.h_kv + kGroups - 1) / kGroups);
+    int64_t want = 8LL * resident / a.tokens;  // warps a token: eight rounds and more even out the last one
+    if (want > steps) want = steps;
+    a.warps_per_token = want >= 8 ? 8 : want >= 4 ? 4 : want >= 2 ? 2 : 1;
+    const int parts = want > 8 ? (int)((want + 7) / 8) : 1;
+    const int64_t per_block = kWarps / a.warps_per_token, blocks = (a.tokens + per_block - 1) / per_block;
+    return gdndev::launch_pdl(a.pairs ? qk_norm_rope<BF16, D, true> : qk_norm_rope<BF16, D, false>, dim3((unsigned)blocks, parts),
+                              dim3(kThreads), 0, st, a) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
 }  // namespace

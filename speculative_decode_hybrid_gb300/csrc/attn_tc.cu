@@ -38,7 +38,9 @@
 namespace {
 
 using gdnattn::AttnArgs;
+using gdndev::add2;
 using gdndev::Buf;
+using gdndev::fma2;
 
 constexpr int kM = 128;                    // rows of an M tile
 constexpr unsigned long long kGiveUpNs = 1000000000ull;  // a wait's limit
@@ -192,22 +194,6 @@ __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
-}
-__device__ __forceinline__ float2 fma2(float2 x, float2 y, float2 z) {
-    float2 r;
-    asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
-        "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
-        : "=f"(r.x), "=f"(r.y)
-        : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y), "f"(z.x), "f"(z.y));
-    return r;
-}
-__device__ __forceinline__ float2 add2(float2 x, float2 y) {
-    float2 r;
-    asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
-        "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
-        : "=f"(r.x), "=f"(r.y)
-        : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y));
-    return r;
 }
 __device__ __forceinline__ unsigned pack_bf16(float lo, float hi) {
     unsigned r;
