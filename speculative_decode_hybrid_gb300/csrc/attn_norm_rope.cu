@@ -32,7 +32,9 @@ using gdndev::mul2;
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kBlocksPerSm = 4;
+// What the registers leave room for: with a fourth block the f32 form spills (31 us
+// instead of 19 for 4,000 tokens of 24 heads of 128).
+constexpr int blocks_per_sm(bool bf16) { return bf16 ? 4 : 3; }
 
 struct RopeArgs {
     int n_tok, h_q, h_kv, page_shift, n_pages, width, rot, max_pos, warps_per_token;
@@ -100,7 +102,7 @@ __device__ __forceinline__ Run<BF16> narrow(const float2 (&x)[2]) {
 // grid (token blocks, parts): a block's eight warps are 8 / warps_per_token
 // tokens; with several parts a token's warps are spread over as many blocks.
 template <bool BF16, int D, bool PAIRS>
-__global__ void __launch_bounds__(kThreads, kBlocksPerSm) qk_norm_rope(RopeArgs a) {
+__global__ void __launch_bounds__(kThreads, blocks_per_sm(BF16)) qk_norm_rope(RopeArgs a) {
     constexpr int kLanes = D / 8, kGroups = 32 / kLanes, kElem = BF16 ? 2 : 4, kRun = 4 * kElem, kHead = D * kElem;
     constexpr int kAhead = BF16 ? 4 : 2;  // steps whose loads are in flight together
     const int lane = threadIdx.x % kLanes, group = threadIdx.x % 32 / kLanes, warp = threadIdx.x / 32;
@@ -218,7 +220,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) qk_norm_rope(RopeArgs 
                     out[0] = narrow<BF16>(x);
                     out[1] = narrow<BF16>(y);
                 }
-                char *p = to + (size_t)h * to_step;
+                char *p = to + h * to_step;
                 if (h < count && GDN_IN(p + d0, kRun, bto, st) && GDN_IN(p + d1, kRun, bto, st))
                     store_run<BF16>(p + d0, out[0]), store_run<BF16>(p + d1, out[1]);
             }
@@ -239,7 +241,7 @@ int launch(RopeArgs a, cudaStream_t st) {
     constexpr int kGroups = 32 / (D / 8);
     // many tokens: a warp each, as long as that fills the GPU; few: up to a warp
     // for every step
-    const int sms = gdnhost::sm_count(), resident = kBlocksPerSm * kWarps * (sms > 0 ? sms : 152);
+    const int sms = gdnhost::sm_count(), resident = blocks_per_sm(BF16) * kWarps * (sms > 0 ? sms : 152);
     const int steps = (a.h_q + kGroups - 1) / kGroups + 2 * ((a.h_kv + kGroups - 1) / kGroups);
     int64_t want = 8LL * resident / a.tokens;  // warps a token: eight rounds and more even out the last one
     if (want > steps) want = steps;

@@ -24,10 +24,36 @@ constexpr int kMaxNodes = GDN_MAX_TOKENS + 1;
 
 // ---------------------------------------------------------------- commit
 
-struct CommitArgs {
-    int n_nodes, layers, h_kv, page_shift, n_pages, width, row_units;  // row_units: 16-byte units of one row
-    const int32_t *parent, *node, *ctx, *table;
+// x / n by a multiplication with 2^32 / n rounded up (x * n < 2^32; n == 1 is 0).
+__host__ __device__ __forceinline__ unsigned reciprocal(unsigned n) { return (unsigned)(((1ull << 32) + n - 1) / n); }
+__device__ __forceinline__ int quotient(int x, unsigned by) { return by ? (int)__umulhi((unsigned)x, by) : x; }
+
+// Where the slices (pool, layer, head) of the two pools lie.
+struct Slices {
     uint4 *k, *v;
+    int layers, h_kv;
+    unsigned by_h_kv;
+    size_t layer_units, head_units;  // 16-byte units of a layer's pool, of one page and head
+    __device__ __forceinline__ uint4 *at(int s) const {
+        const int pl = quotient(s, by_h_kv), head = s - pl * h_kv, layer = pl < layers ? pl : pl - layers;
+        return (pl < layers ? k : v) + layer * layer_units + head * head_units;
+    }
+    // a row of page p at offset o of slice 0
+    __device__ __forceinline__ size_t row(int p, int o, int row_units) const {
+        return (size_t)p * h_kv * head_units + (size_t)o * row_units;
+    }
+};
+
+Slices slices_of(const attn_dims *d, void *k, void *v) {
+    const size_t head = (size_t)d->page_tokens * d->d_head * gdnhost::attn_elem_bytes(d) / 16;
+    return {static_cast<uint4 *>(k), static_cast<uint4 *>(v), d->layers, d->h_kv, reciprocal(d->h_kv),
+            head * d->h_kv * d->n_pages, head};
+}
+
+struct CommitArgs {
+    int n_nodes, page_shift, n_pages, width, unit_shift;  // 2^unit_shift 16-byte units are a row
+    Slices slices;
+    const int32_t *parent, *node, *ctx, *table;
     int32_t *ctx_out, *status;
 };
 
@@ -39,16 +65,16 @@ constexpr int kCommitHold = 8;  // 16-byte units a thread holds between the read
 // nodes' sources, so a slice is read whole before it is written: a round takes
 // as many slices as the threads' registers hold (at least one: a path of 64
 // rows of 1 KB goes in column ranges).
-__global__ void __launch_bounds__(kCommitThreads) commit_path(CommitArgs a) {
+__global__ void __launch_bounds__(kCommitThreads, 4) commit_path(CommitArgs a) {
     __shared__ int32_t parent[kMaxNodes];
     __shared__ int depth_of_last, in_place;
-    __shared__ long long src_row[GDN_MAX_TOKENS], dst_row[GDN_MAX_TOKENS];  // page * page_tokens * h_kv + offset; -1: no such page
+    __shared__ long long src_row[GDN_MAX_TOKENS], dst_row[GDN_MAX_TOKENS];  // in units from a slice's begin; -1: no such page
     const int b = blockIdx.y, tid = threadIdx.x, N = a.n_nodes;
     const size_t B = gridDim.y;
     int32_t *st = a.status;
     const Buf bp{a.parent, B * N * 4}, bt{a.table, B * (size_t)a.width * 4};
-    const size_t slice_units = (size_t)a.row_units << a.page_shift;  // of one page and head
-    const size_t pool_bytes = (size_t)a.layers * a.n_pages * a.h_kv * slice_units * 16;
+    const int row_units = 1 << a.unit_shift;
+    const Buf bk{a.slices.k, a.slices.layers * a.slices.layer_units * 16}, bv{a.slices.v, a.slices.layers * a.slices.layer_units * 16};
     gdndev::pdl_wait();
     const int node = a.node[b], ctx = a.ctx[b];
     const bool fits = ctx >= 0 && (int64_t)ctx + N - 1 <= (int64_t)a.width << a.page_shift;
@@ -86,8 +112,8 @@ __global__ void __launch_bounds__(kCommitThreads) commit_path(CommitArgs a) {
                 const int mask = (1 << a.page_shift) - 1;
                 const bool okS = ps >= 0 && ps < a.n_pages, okD = pd >= 0 && pd < a.n_pages;
                 if ((!okS || !okD) && blockIdx.x == 0 && st) atomicOr(st, GDN_DEV_PAGE);
-                src_row[depth - 1] = okS ? ((long long)ps * a.h_kv << a.page_shift) + (s & mask) : -1;
-                dst_row[depth - 1] = okD ? ((long long)pd * a.h_kv << a.page_shift) + (d & mask) : -1;
+                src_row[depth - 1] = okS ? (long long)a.slices.row(ps, s & mask, row_units) : -1;
+                dst_row[depth - 1] = okD ? (long long)a.slices.row(pd, d & mask, row_units) : -1;
             }
         }
         __syncthreads();
@@ -103,28 +129,33 @@ __global__ void __launch_bounds__(kCommitThreads) commit_path(CommitArgs a) {
     if (!a.parent) return;
     const int first = in_place, rows = k - first;
     if (rows <= 0) return;
-    const int slices = 2 * a.layers * a.h_kv, parts = gridDim.x;
+    const int slices = 2 * a.slices.layers * a.slices.h_kv, parts = gridDim.x;
     const int s0 = (int)((long long)slices * blockIdx.x / parts), s1 = (int)((long long)slices * (blockIdx.x + 1) / parts);
-    // a round: `group` slices of `cols` units of each row
+    // a round: `group` slices of 2^col_shift units of each row
     constexpr int kUnits = kCommitThreads * kCommitHold;
-    const int cols = min(a.row_units, kUnits / rows), group = max(1, kUnits / (rows * a.row_units));
+    int col_shift = a.unit_shift;
+    while (rows << col_shift > kUnits) --col_shift;
+    const int group = max(1, kUnits / (rows << col_shift));
+    const unsigned by_rows = reciprocal(rows);
     for (int s = s0; s < s1; s += group)
-        for (int c0 = 0; c0 < a.row_units; c0 += cols) {
-            const int nc = min(cols, a.row_units - c0), ng = min(group, s1 - s), items = ng * rows * nc;
+        for (int c0 = 0; c0 < row_units; c0 += 1 << col_shift) {
+            const int items = min(group, s1 - s) * rows << col_shift;
             uint4 held[kCommitHold];
+            // item -> slice, row, column
+            auto place = [&](int it, const long long *row_of, Buf &buf) -> uint4 * {
+                const int r = it >> col_shift, sl = quotient(r, by_rows);
+                const long long at = row_of[first + r - sl * rows];
+                buf = s + sl < slices / 2 ? bk : bv;
+                return at < 0 ? nullptr : a.slices.at(s + sl) + at + c0 + (it & ((1 << col_shift) - 1));
+            };
 #pragma unroll
             for (int h = 0; h < kCommitHold; ++h) {
                 const int it = tid + h * kCommitThreads;
                 held[h] = make_uint4(0, 0, 0, 0);
                 if (it < items) {
-                    const int col = c0 + it % nc, row = first + it / nc % rows, sl = s + it / (nc * rows);
-                    const int head = sl % a.h_kv, layer = sl / a.h_kv % a.layers, pool = sl / (a.h_kv * a.layers);
-                    const long long r = src_row[row];
-                    if (r >= 0) {
-                        const uint4 *f = (pool ? a.v : a.k) + ((size_t)layer * a.n_pages * a.h_kv << a.page_shift) * a.row_units +
-                                         ((size_t)r + ((size_t)head << a.page_shift)) * a.row_units + col;
-                        if (GDN_IN(f, 16, (Buf{(pool ? a.v : a.k), pool_bytes}), st)) held[h] = *f;
-                    }
+                    Buf buf;
+                    const uint4 *f = place(it, src_row, buf);
+                    if (f && GDN_IN(f, 16, buf, st)) held[h] = *f;
                 }
             }
             __syncthreads();
@@ -132,14 +163,9 @@ __global__ void __launch_bounds__(kCommitThreads) commit_path(CommitArgs a) {
             for (int h = 0; h < kCommitHold; ++h) {
                 const int it = tid + h * kCommitThreads;
                 if (it < items) {
-                    const int col = c0 + it % nc, row = first + it / nc % rows, sl = s + it / (nc * rows);
-                    const int head = sl % a.h_kv, layer = sl / a.h_kv % a.layers, pool = sl / (a.h_kv * a.layers);
-                    const long long r = dst_row[row];
-                    if (r >= 0) {
-                        uint4 *f = (pool ? a.v : a.k) + ((size_t)layer * a.n_pages * a.h_kv << a.page_shift) * a.row_units +
-                                   ((size_t)r + ((size_t)head << a.page_shift)) * a.row_units + col;
-                        if (GDN_IN(f, 16, (Buf{(pool ? a.v : a.k), pool_bytes}), st)) *f = held[h];
-                    }
+                    Buf buf;
+                    uint4 *f = place(it, dst_row, buf);
+                    if (f && GDN_IN(f, 16, buf, st)) *f = held[h];
                 }
             }
         }
@@ -281,10 +307,10 @@ __global__ void __launch_bounds__(kPoolThreads) resize_pages(ResizeArgs a) {
 }
 
 struct ForkArgs {
-    int batch, n_fork, width, page_shift, n_pages, layers, h_kv, row_units;
+    int batch, n_fork, width, page_shift, n_pages, row_units;
+    Slices slices;
     const int32_t *src, *dst;
     int32_t *table, *ctx, *ref;
-    uint4 *k, *v;
     int32_t *fresh;  // [n_fork] page taken for the tail; -1 none needed, -2 left out, -3 no page left
     int32_t *list;
     int32_t *status;
@@ -343,8 +369,7 @@ __global__ void __launch_bounds__(kForkThreads) fork_copy(ForkArgs a) {
     int32_t *st = a.status;
     const size_t B = a.batch;
     const Buf bt{a.table, B * (size_t)a.width * 4}, br{a.ref, (size_t)a.n_pages * 4};
-    const size_t slice_units = (size_t)a.row_units << a.page_shift;
-    const size_t pool_bytes = (size_t)a.layers * a.n_pages * a.h_kv * slice_units * 16;
+    const Buf bk{a.slices.k, a.slices.layers * a.slices.layer_units * 16}, bv{a.slices.v, a.slices.layers * a.slices.layer_units * 16};
     gdndev::pdl_wait();
     const int fresh = a.fresh[i];
     if (fresh == -2) return;
@@ -371,23 +396,30 @@ __global__ void __launch_bounds__(kForkThreads) fork_copy(ForkArgs a) {
     const int old = GDN_IN(from + full, 4, bt, st) ? from[full] : -1;
     const bool known = old >= 0 && old < a.n_pages;
     if (!known && blockIdx.x == 0 && tid == 0 && st) atomicOr(st, GDN_DEV_PAGE);
-    const int slices = 2 * a.layers * a.h_kv, parts = gridDim.x, units = tail * a.row_units;
-    const long long all = (long long)slices * units;
-    for (long long it = (long long)blockIdx.x * kForkThreads + tid; it < all; it += (long long)parts * kForkThreads) {
-        const int sl = (int)(it / units), u = (int)(it % units);
-        const int head = sl % a.h_kv, layer = sl / a.h_kv % a.layers, pool = sl / (a.h_kv * a.layers);
-        uint4 *base = (pool ? a.v : a.k) + (size_t)layer * a.n_pages * a.h_kv * slice_units;
-        const uint4 *f = base + ((size_t)old * a.h_kv + head) * slice_units + u;
-        uint4 *t = base + ((size_t)fresh * a.h_kv + head) * slice_units + u;
-        const Buf bpool{(pool ? a.v : a.k), pool_bytes};
-        const uint4 v = known && GDN_IN(f, 16, bpool, st) ? *f : make_uint4(0, 0, 0, 0);
-        if (GDN_IN(t, 16, bpool, st)) *t = v;
+    const int slices = 2 * a.slices.layers * a.slices.h_kv, units = tail * a.row_units;
+    const size_t from_row = a.slices.row(known ? old : 0, 0, a.row_units), to_row = a.slices.row(fresh, 0, a.row_units);
+    for (int s = blockIdx.x; s < slices; s += gridDim.x) {
+        uint4 *slice = a.slices.at(s);
+        const Buf buf = s < slices / 2 ? bk : bv;
+        for (int u0 = tid; u0 < units; u0 += 4 * kForkThreads) {
+            uint4 x[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int u = u0 + j * kForkThreads;
+                x[j] = known && u < units && GDN_IN(slice + from_row + u, 16, buf, st) ? slice[from_row + u] : make_uint4(0, 0, 0, 0);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int u = u0 + j * kForkThreads;
+                if (u < units && GDN_IN(slice + to_row + u, 16, buf, st)) slice[to_row + u] = x[j];
+            }
+        }
     }
 }
 
-int page_shift(int page_tokens) {
+int log2_of(int n) {
     int s = 0;
-    while ((1 << s) < page_tokens) ++s;
+    while ((1 << s) < n) ++s;
     return s;
 }
 
@@ -413,9 +445,9 @@ extern "C" int kv_commit_path(const attn_dims *dims, int32_t n_nodes, const int3
     for (const void *p : {(const void *)parent_dev, (const void *)accept_node, (const void *)ctx_len,
                           (const void *)page_table, (const void *)ctx_out, (const void *)dev_status})
         if (!aligned_to(p, 4)) return GDN_ERR_ALIGN;
-    CommitArgs a{n_nodes, dims->layers, dims->h_kv, page_shift(dims->page_tokens), dims->n_pages, dims->table_width,
-                 (int)(dims->d_head * gdnhost::attn_elem_bytes(dims) / 16), parent_dev, accept_node, ctx_len, page_table,
-                 static_cast<uint4 *>(k_pages), static_cast<uint4 *>(v_pages), ctx_out, dev_status};
+    CommitArgs a{n_nodes, log2_of(dims->page_tokens), dims->n_pages, dims->table_width,
+                 log2_of((int)(dims->d_head * gdnhost::attn_elem_bytes(dims) / 16)), slices_of(dims, k_pages, v_pages),
+                 parent_dev, accept_node, ctx_len, page_table, ctx_out, dev_status};
     const int64_t slices = 2LL * dims->layers * dims->h_kv;
     const int parts = parent_dev ? parts_for(dims->batch, slices < 65535 ? (int)slices : 65535) : 1;
     return gdndev::launch_pdl(commit_path, dim3(parts, dims->batch), dim3(kCommitThreads), 0,
@@ -445,7 +477,7 @@ extern "C" int kv_pages_resize(const attn_dims *dims, const int32_t *want, int32
     if (const int rc = check_pages(dims, {want, page_table, page_ref}, workspace, workspace_bytes, dev_status)) return rc;
     int32_t *need = static_cast<int32_t *>(workspace);
     int32_t *list = reinterpret_cast<int32_t *>(static_cast<char *>(workspace) + round256((size_t)dims->batch * 4));
-    ResizeArgs a{dims->batch, dims->table_width, page_shift(dims->page_tokens), dims->n_pages, want, page_table, page_ref,
+    ResizeArgs a{dims->batch, dims->table_width, log2_of(dims->page_tokens), dims->n_pages, want, page_table, page_ref,
                  need, list, dev_status};
     return gdndev::launch_pdl(resize_pages, dim3(1), dim3(kPoolThreads), 0, static_cast<cudaStream_t>(stream), a) ==
                    cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
@@ -462,9 +494,9 @@ extern "C" int kv_pages_fork(const attn_dims *dims, int32_t n_fork, const int32_
     if (!gdnhost::aligned_to(k_pages, 16) || !gdnhost::aligned_to(v_pages, 16)) return GDN_ERR_ALIGN;
     int32_t *fresh = static_cast<int32_t *>(workspace);
     int32_t *list = reinterpret_cast<int32_t *>(static_cast<char *>(workspace) + round256((size_t)dims->batch * 4));
-    ForkArgs a{dims->batch, n_fork, dims->table_width, page_shift(dims->page_tokens), dims->n_pages, dims->layers,
-               dims->h_kv, (int)(dims->d_head * gdnhost::attn_elem_bytes(dims) / 16), src, dst, page_table, ctx_len,
-               page_ref, static_cast<uint4 *>(k_pages), static_cast<uint4 *>(v_pages), fresh, list, dev_status};
+    ForkArgs a{dims->batch, n_fork, dims->table_width, log2_of(dims->page_tokens), dims->n_pages,
+               (int)(dims->d_head * gdnhost::attn_elem_bytes(dims) / 16), slices_of(dims, k_pages, v_pages), src, dst,
+               page_table, ctx_len, page_ref, fresh, list, dev_status};
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (gdndev::launch_pdl(fork_take, dim3(1), dim3(kPoolThreads), 0, s, a) != cudaSuccess) return GDN_ERR_CUDA;
     const int64_t slices = 2LL * dims->layers * dims->h_kv;
