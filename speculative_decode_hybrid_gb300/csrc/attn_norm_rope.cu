@@ -119,6 +119,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(BF16)) qk_norm_rope(Ro
     const bool turned = PAIRS ? lane * 8 < a.rot : lane * 4 < half;
     const int d0 = (turned && !PAIRS ? lane * 4 : lane * 8) * kElem, d1 = (turned && !PAIRS ? half + lane * 4 : lane * 8 + 4) * kElem;
     gdndev::pdl_wait();
+    gdndev::pdl_launch_dependents();
     if (token >= a.tokens) return;
     const int b = (int)((unsigned)token / (unsigned)a.n_tok), t = (int)token - b * a.n_tok + 1;
     const int ctx = a.ctx[b];

@@ -175,6 +175,7 @@ __global__ void __launch_bounds__(256) join_parts(AttnArgs a, int parts, const f
     int32_t *st = a.status;
     const Buf bo{part_o, (size_t)rows * parts * D * 4}, bms{part_ms, (size_t)rows * parts * 8}, bout{a.out, (size_t)rows * D * kElem};
     gdndev::pdl_wait();
+    gdndev::pdl_launch_dependents();
     if (row >= rows) return;
     float m = -INFINITY;
     for (int p = lane; p < parts; p += 32) {

@@ -195,6 +195,11 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+__device__ __forceinline__ float max3(float x, float y, float z) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+    return r;
+}
 __device__ __forceinline__ unsigned pack_bf16(float lo, float hi) {
     unsigned r;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -249,6 +254,8 @@ attend(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtens
     constexpr int kTmaWarp = W * 4, kScoreWarp = W * 4 + 1, kSumWarp = W * 4 + 2;
 
     if (warp == kScoreWarp) gdntc::tmem_alloc<kTmemCols>(&c.tmem);
+    if (warp == kTmaWarp && lane < 2)
+        asm volatile("prefetch.tensormap [%0];" ::"l"(lane ? &v_map : &k_map) : "memory");
     if (tid == 0) {
         for (int i = 0; i < kStages; ++i) {
             bar_init(saddr(&c.k_full[i]), 1);
@@ -480,6 +487,9 @@ attend(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtens
             } else {
                 gdntc::fence_smem_to_async();
             }
+            if (w == 0 && row_in_tile == 0) c.odd_nodes[(seg + 1) & 3] = 0;
+            __syncwarp();
+            if (lane == 0) bar_arrive(saddr(&c.q_full));
             if (work.left > 0) {  // the next segment's queries on their way to L2
                 Work peek = work;
                 const Segment n = next_segment<kN>(a, plan, peek);
@@ -487,9 +497,6 @@ attend(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtens
                 if (r < rows)
                     gdndev::prefetch_l2_range(static_cast<const __nv_bfloat16 *>(a.q) + row_offset(a, plan, n.b, nkv, r) * D, D * 2, 0, 1);
             }
-            if (w == 0 && row_in_tile == 0) c.odd_nodes[(seg + 1) & 3] = 0;
-            __syncwarp();
-            if (lane == 0) bar_arrive(saddr(&c.q_full));
             unsigned long long path = 0;
             if ((s.tile0 + s.n) * kN > ctx && live) {  // a tile with drafted slots
                 const int t = quotient(row, plan.by_group) + 1;
@@ -539,7 +546,8 @@ attend(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtens
 #pragma unroll
                     for (int k = 0; k < kN / 32; ++k)
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) tops[i & 7] = fmaxf(tops[i & 7], __uint_as_float(x[k][i]));
+                        for (int i = 0; i < 32; i += 2)
+                            tops[i / 2 & 7] = max3(tops[i / 2 & 7], __uint_as_float(x[k][i]), __uint_as_float(x[k][i + 1]));
                     float top = fmaxf(fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])),
                                       fmaxf(fmaxf(tops[4], tops[5]), fmaxf(tops[6], tops[7])));
                     if (j == 0) {
@@ -728,6 +736,7 @@ join_pieces(const __grid_constant__ AttnArgs a, const __grid_constant__ Plan pla
     const Buf bo{pieces.o, (size_t)2 * plan.blocks * kRows * D * 4}, bms{pieces.ms, (size_t)2 * plan.blocks * kRows * 8},
         bout{a.out, (size_t)a.batch * a.n_tok * a.h_q * D * 2};
     gdndev::pdl_wait();
+    gdndev::pdl_launch_dependents();
     // the unit's pieces, from the blocks' notes
     int note[kNotes], unit = index;
 #pragma unroll

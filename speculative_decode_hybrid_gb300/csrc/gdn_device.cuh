@@ -38,7 +38,10 @@ __device__ __forceinline__ bool in_buf(const void *ptr, size_t n, Buf b, int32_t
 // writes are visible; returns at once for a grid launched without the
 // attribute. Every kernel of this library calls it before its first global
 // memory access. pdl_launch_dependents(): let the grid launched after this
-// one be scheduled now (it still waits for this grid's completion).
+// one be scheduled now (it still waits for this grid's completion). The last
+// kernel of a call does so only after its own wait: a caller's next kernel may
+// rely on everything before the kernel it overlaps being complete
+// (GDN_VERIFY_STATE_READY).
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 

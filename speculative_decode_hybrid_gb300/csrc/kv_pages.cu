@@ -76,6 +76,7 @@ __global__ void __launch_bounds__(kCommitThreads, 4) commit_path(CommitArgs a) {
     const int row_units = 1 << a.unit_shift;
     const Buf bk{a.slices.k, a.slices.layers * a.slices.layer_units * 16}, bv{a.slices.v, a.slices.layers * a.slices.layer_units * 16};
     gdndev::pdl_wait();
+    gdndev::pdl_launch_dependents();
     const int node = a.node[b], ctx = a.ctx[b];
     const bool fits = ctx >= 0 && (int64_t)ctx + N - 1 <= (int64_t)a.width << a.page_shift;
     const bool known = node >= 0 && node < N;
@@ -242,6 +243,7 @@ __global__ void __launch_bounds__(kPoolThreads) resize_pages(ResizeArgs a) {
     const Buf bt{a.table, B * (size_t)a.width * 4}, br{a.ref, (size_t)a.n_pages * 4}, bneed{a.need, B * 4},
         blist{a.list, (size_t)a.n_pages * 4};
     gdndev::pdl_wait();
+    gdndev::pdl_launch_dependents();
     // one warp per request: entries past the wanted length are given back, the
     // missing ones below it counted
     for (int b = warp; b < a.batch; b += kPoolWarps) {
@@ -371,6 +373,7 @@ __global__ void __launch_bounds__(kForkThreads) fork_copy(ForkArgs a) {
     const Buf bt{a.table, B * (size_t)a.width * 4}, br{a.ref, (size_t)a.n_pages * 4};
     const Buf bk{a.slices.k, a.slices.layers * a.slices.layer_units * 16}, bv{a.slices.v, a.slices.layers * a.slices.layer_units * 16};
     gdndev::pdl_wait();
+    gdndev::pdl_launch_dependents();
     const int fresh = a.fresh[i];
     if (fresh == -2) return;
     const int s = a.src[i], d = a.dst[i], n = fresh == -3 ? 0 : a.ctx[s];

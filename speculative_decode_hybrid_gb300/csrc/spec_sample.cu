@@ -275,6 +275,7 @@ sample_pick(PickArgs a) {
         more_after[tid] = more;
     }
     gdndev::pdl_wait();
+    gdndev::pdl_launch_dependents();
     for (int n = warp; n < N; n += kPickThreads / 32) {
         const Stat *row = a.stats + ((size_t)b * N + n) * kMaxPieces;
         Stat s[2];  // kMaxPieces is at most 64
