@@ -2,10 +2,9 @@
 // (attn_verify_span / attn_tree_verify with GDN_BF16).
 //
 // The rows of one key/value head's product are the span's nodes times the query
-// heads of the group: 128 rows are one M tile, and a block holds W of them
-// (two, where the head is at most 128 wide and there are more than 128 rows).
-// For each tile of kN slots
-//   S = Q K^T        tcgen05, operands in shared memory, S in tensor memory
+// heads of the group; 128 of them are an M tile, the work of one block. For each
+// tile of kN slots
+//   S = Q K^T        tcgen05, Q in tensor memory, K in shared memory, S in tensor memory
 //   P = 2^(c S - m)  one thread per row, rounded to bf16, over S's columns
 //   O += P V         tcgen05, P read from tensor memory, V MN-major in shared
 //                    memory as it lies in the page
@@ -14,9 +13,14 @@
 // memory): the weights stay below 2^8, and the final division by the sum of
 // the same weights makes the result independent of m.
 //
-// Warps: 4 per M tile for the softmax, one that keeps the TMA loads of the next
-// tiles in flight (a page's rows of one head are a box of a 3-d tensor map, so
-// a tile is gathered page by page), one that issues each of the products.
+// Warps: 4 for the softmax, one that keeps the TMA loads of the next tiles in
+// flight (a page's rows of one head are a box of a 3-d tensor map, so a tile is
+// gathered page by page), one that issues each of the products. S is double:
+// the scores of the next tile are computed while the softmax works on this one.
+//
+// More than 128 rows: clusters of P = 2 blocks, an M tile each, over the same
+// tiles; each block loads half of a tile's boxes into both (TMA multicast), so
+// that what leaves L2 is read once.
 //
 // Work is split over the whole flattened list of (request, head, M tiles, slot
 // tile): block i of n takes the i-th n-th of it, whatever the requests'
@@ -24,8 +28,8 @@
 // join_pieces adds them up on the scale of their largest maximum.
 //
 // Bound by the bytes of K and V while the rows are few (4 kN D bytes a tile
-// against 2 x 128 x kN x D x 2 W operations), and by the exponentials once two
-// M tiles are full.
+// against 4 x 128 x kN x D operations), by products and exponentials with full
+// M tiles.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -48,29 +52,24 @@ constexpr unsigned long long kGiveUpNs = 1000000000ull;  // a wait's limit
 constexpr int kTmemCols = 512;  // all of an SM's: one block per SM
 constexpr int kMaxBlocks = 160, kNotes = 2 * kMaxBlocks / 32;
 
-template <int D, int W>
+template <int D>
 struct Shape {
     static constexpr int kN = D == 256 ? 64 : 128;       // slots of a tile
     static constexpr int kChunks = D / 64;               // 128-byte column chunks of a row
-    static constexpr int kSlots = 2;                     // S buffers: one per M tile, or two in turn
-    static constexpr unsigned kSCol = W * D, kQCol = kSCol + kSlots * kN;  // tensor-memory columns: O, S, Q
-    // Q is read from tensor memory where it fits beside O and S: a product then
-    // reads half as much shared memory
-    static constexpr bool kQInTmem = kQCol + W * D / 2 <= kTmemCols;
-    static constexpr int kStages = D == 64 ? 6 : kQInTmem ? 3 : 2;
+    static constexpr unsigned kSCol = D, kQCol = kSCol + 2 * kN;  // tensor-memory columns: O, S twice, Q
+    static constexpr int kStages = D == 64 ? 6 : 3;
     static constexpr unsigned kTileBytes = kN * D * 2;   // of K, and of V
-    static constexpr unsigned kQBytes = kQInTmem ? 0 : kM * D * 2;  // of one M tile in shared memory
-    static constexpr unsigned kPassBytes = kQInTmem ? W * 4 * 4096 : 0;  // a warp's 32 rows x 128 bytes of Q on their way
-    static constexpr int kThreads = W * 128 + 96;
-    static constexpr unsigned kSmem = W * kQBytes + 2 * kStages * kTileBytes + kPassBytes + 1024;
-    static_assert(kQCol <= kTmemCols, "tensor memory");
+    static constexpr unsigned kPassBytes = 4 * 4096;     // a warp's 32 rows x 128 bytes of Q on their way
+    static constexpr int kThreads = 128 + 96;
+    static constexpr unsigned kSmem = 2 * kStages * kTileBytes + kPassBytes + 1024;
+    static_assert(kQCol + D / 2 <= kTmemCols, "tensor memory");
 };
 
 // What the host works out: divisions take a warp longer than a load from L2.
 struct Plan {
     int group, rows;        // query heads of a key/value head; rows of one key/value head
-    int m_groups, units;    // groups of W M tiles of a head; units (head, group) of a request
-    int blocks;
+    int m_groups, units;    // groups of P M tiles of a head; units (head, group) of a request
+    int blocks;             // clusters of P blocks
     unsigned by_group, by_m_groups, by_blocks;  // 2^32 / n rounded up: x / n for x * n < 2^32
 };
 
@@ -119,7 +118,7 @@ struct Share {
 // This block's share, and the request in which it begins: by each warp for
 // itself, so that none waits for another.
 template <int kN>
-__device__ __forceinline__ Work block_work(const AttnArgs &a, const Plan &plan, bool flag) {
+__device__ __forceinline__ Work block_work(const AttnArgs &a, const Plan &plan, int block, bool flag) {
     const int lane = threadIdx.x & 31;
     auto tiles_of = [&](int b) { return b < a.batch ? (gdnattn::slots_of(a, b) + kN - 1) / kN : 0; };
     const int mine = tiles_of(lane);
@@ -127,7 +126,7 @@ __device__ __forceinline__ Work block_work(const AttnArgs &a, const Plan &plan, 
     for (int b0 = 0; b0 < a.batch; b0 += 32) total += __reduce_add_sync(~0u, b0 ? tiles_of(b0 + lane) : mine);
     const int units = plan.units;
     const Share share(total * units, plan.blocks);
-    const long long lo = share.start(blockIdx.x, plan), hi = share.start(blockIdx.x + 1, plan);
+    const long long lo = share.start(block, plan), hi = share.start(block + 1, plan);
     Work w{0, 0, 0};
     long long before = 0;
     for (int b0 = 0; b0 < a.batch && (lo >= before || flag); b0 += 32) {
@@ -189,6 +188,17 @@ __device__ __forceinline__ void load_box(unsigned dst, const CUtensorMap *map, i
         "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
         : "memory");
 }
+// Into both blocks of a cluster of two, at this place, and counted by the barrier there.
+__device__ __forceinline__ void load_box_pair(unsigned dst, const CUtensorMap *map, int x, int y, int z, unsigned bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster [%0], [%1, {%2, %3, "
+        "%4}], [%5], %6;" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar), "h"((unsigned short)3)
+        : "memory");
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -223,14 +233,14 @@ __device__ __forceinline__ size_t row_offset(const AttnArgs &a, const Plan &plan
 }
 
 struct Pieces {
-    float4 *o;    // [2 blocks][D / 4][W * 128]
-    float2 *ms;   // [2 blocks][W * 128]: reference maximum in powers of two, sum
+    float4 *o;    // [2 blocks][D / 4][P * 128]
+    float2 *ms;   // [2 blocks][P * 128]: reference maximum in powers of two, sum
     int *unit;    // [2 blocks]: request * units + unit of a block's first and last piece of a shared unit, -1 for none
 };
 
-template <int D, int W>
+template <int D>
 struct Control {
-    static constexpr int kStages = Shape<D, W>::kStages;
+    static constexpr int kStages = Shape<D>::kStages;
     unsigned long long k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
     unsigned long long s_full[2], p_full[2], pv_done[2], q_full, drain[2];
     unsigned long long odd_nodes[4];  // drafted nodes with a value of v that is no number, by segment
@@ -238,20 +248,21 @@ struct Control {
     int quit;
 };
 
-template <int D, int W>
-__global__ void __launch_bounds__(Shape<D, W>::kThreads, 1)
+template <int D, int P>
+__global__ void __launch_bounds__(Shape<D>::kThreads, 1)
 attend(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
        const __grid_constant__ AttnArgs a, const __grid_constant__ Plan plan, const __grid_constant__ Pieces pieces) {
-    using S = Shape<D, W>;
+    using S = Shape<D>;
     constexpr int kN = S::kN, kStages = S::kStages;
     extern __shared__ char raw[];
-    __shared__ Control<D, W> c;
+    __shared__ Control<D> c;
     char *base = raw + ((1024 - (saddr(raw) & 1023)) & 1023);
-    const unsigned q_s = saddr(base), k_s = q_s + W * S::kQBytes, v_s = k_s + kStages * S::kTileBytes, pass_s = v_s + kStages * S::kTileBytes;
+    const unsigned k_s = saddr(base), v_s = k_s + kStages * S::kTileBytes, pass_s = v_s + kStages * S::kTileBytes;
+    const int cluster = blockIdx.x / P, rank = blockIdx.x % P;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int group = plan.group, rows = plan.rows;
     int32_t *st = a.status;
-    constexpr int kTmaWarp = W * 4, kScoreWarp = W * 4 + 1, kSumWarp = W * 4 + 2;
+    constexpr int kTmaWarp = 4, kScoreWarp = 5, kSumWarp = 6;
 
     if (warp == kScoreWarp) gdntc::tmem_alloc<kTmemCols>(&c.tmem);
     if (warp == kTmaWarp && lane < 2)
@@ -259,16 +270,16 @@ attend(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtens
     if (tid == 0) {
         for (int i = 0; i < kStages; ++i) {
             bar_init(saddr(&c.k_full[i]), 1);
-            bar_init(saddr(&c.k_empty[i]), 1);
+            bar_init(saddr(&c.k_empty[i]), P);  // a stage is free once both blocks have used it
             bar_init(saddr(&c.v_full[i]), 1);
-            bar_init(saddr(&c.v_empty[i]), 1);
+            bar_init(saddr(&c.v_empty[i]), P);
         }
         for (int i = 0; i < 2; ++i) {
             bar_init(saddr(&c.s_full[i]), 1);
             bar_init(saddr(&c.p_full[i]), 4);  // one arrival per softmax warp
             bar_init(saddr(&c.pv_done[i]), 1);
         }
-        bar_init(saddr(&c.q_full), W * 4);
+        bar_init(saddr(&c.q_full), 4);
         bar_init(saddr(&c.drain[0]), 1);
         bar_init(saddr(&c.drain[1]), 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -277,18 +288,19 @@ attend(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtens
     }
     gdntc::fence_before_sync();
     __syncthreads();
+    if (P == 2) cluster_sync();  // the other block's barriers are there
     gdntc::fence_after_sync();
     const unsigned tmem = c.tmem;
     gdndev::pdl_launch_dependents();
     gdndev::pdl_wait();
-    Work work = block_work<kN>(a, plan, blockIdx.x == 0 && warp == 0);
-    if (tid == 0) pieces.unit[2 * blockIdx.x] = pieces.unit[2 * blockIdx.x + 1] = -1;
+    Work work = block_work<kN>(a, plan, cluster, blockIdx.x == 0 && warp == 0);
+    if (tid == 0 && rank == 0) pieces.unit[2 * cluster] = pieces.unit[2 * cluster + 1] = -1;
     volatile int *quit = &c.quit;
     constexpr unsigned kSCol = S::kSCol, kQCol = S::kQCol;
 
     if (warp == kTmaWarp) {
         int g = 0;  // tiles so far
-        const int page_rows = min(1 << a.page_shift, kN), boxes = kN / page_rows;
+        const int page_rows = min(1 << a.page_shift, kN / P), boxes = kN / page_rows;
         const unsigned box_bytes = page_rows * 128u;
         const int mine = lane / S::kChunks, chunk = lane % S::kChunks;  // this lane's page of the tile, and its column chunk
         const Buf bt{a.table, (size_t)a.batch * a.width * 4};
@@ -324,7 +336,9 @@ attend(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtens
                     if (!ok) break;
                     if (lane == 0) bar_expect(full, bytes);
                     __syncwarp();
-                    if (used) load_box((half ? v_s : k_s) + at, half ? &v_map : &k_map, chunk * 64, y, z, full);
+                    if (P == 1 && used) load_box((half ? v_s : k_s) + at, half ? &v_map : &k_map, chunk * 64, y, z, full);
+                    if (P == 2 && used && (mine & 1) == rank)  // the other boxes come from the other block
+                        load_box_pair((half ? v_s : k_s) + at, half ? &v_map : &k_map, chunk * 64, y, z, full);
                 }
                 if (!ok) break;
                 page = next;
@@ -357,26 +371,18 @@ attend(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtens
                     const int stage = g % kStages;
                     const unsigned k = k_s + stage * S::kTileBytes;
                     ok = wait(saddr(&c.k_full[stage]), (g / kStages) & 1, quit);
-                    for (int w = 0; w < W && ok; ++w) {
-                        const int slot = W == 2 ? w : g & 1;
-                        // the weights that lay in this S buffer have been used
-                        if (W == 2 && g >= 1) ok = wait(saddr(&c.pv_done[w]), (g - 1) & 1, quit);
-                        if (W == 1 && g >= 2) ok = wait(saddr(&c.pv_done[slot]), ((g - 2) >> 1) & 1, quit);
-                        if (!ok) break;
-                        gdntc::fence_after_sync();
+                    // the weights that lay in this S buffer have been used
+                    const int slot = g & 1;
+                    if (g >= 2) ok = ok && wait(saddr(&c.pv_done[slot]), ((g - 2) >> 1) & 1, quit);
+                    if (!ok) break;
+                    gdntc::fence_after_sync();
 #pragma unroll
-                        for (int i = 0; i < D / 16; ++i) {
-                            const uint64_t kd = gdntc::smem_desc_sw128(k + (i / 4) * (kN * 128) + (i % 4) * 32);
-                            if constexpr (S::kQInTmem)
-                                gdntc::mma_bf16_ts(tmem + kSCol + slot * kN, tmem + kQCol + w * (D / 2) + i * 8, kd, kIdS, i > 0);
-                            else
-                                gdntc::mma_bf16_ss(tmem + kSCol + slot * kN,
-                                                   gdntc::smem_desc_sw128(q_s + w * S::kQBytes + (i / 4) * (kM * 128) + (i % 4) * 32),
-                                                   kd, kIdS, i > 0);
-                        }
-                        gdntc::mma_commit(saddr(&c.s_full[slot]));
-                        if (w == W - 1) gdntc::mma_commit(saddr(&c.k_empty[stage]));
-                    }
+                    for (int i = 0; i < D / 16; ++i)
+                        gdntc::mma_bf16_ts(tmem + kSCol + slot * kN, tmem + kQCol + i * 8,
+                                           gdntc::smem_desc_sw128(k + (i / 4) * (kN * 128) + (i % 4) * 32), kIdS, i > 0);
+                    gdntc::mma_commit(saddr(&c.s_full[slot]));
+                    if (P == 2) gdntc::mma_commit_pair(saddr(&c.k_empty[stage]));
+                    else gdntc::mma_commit(saddr(&c.k_empty[stage]));
                 }
             }
             gdntc::mma_commit(saddr(&c.drain[0]));
@@ -395,18 +401,17 @@ attend(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtens
                     const int stage = g % kStages;
                     const unsigned v = v_s + stage * S::kTileBytes;
                     ok = wait(saddr(&c.v_full[stage]), (g / kStages) & 1, quit);
-                    for (int w = 0; w < W && ok; ++w) {
-                        const int slot = W == 2 ? w : g & 1;
-                        ok = wait(saddr(&c.p_full[slot]), W == 2 ? g & 1 : (g >> 1) & 1, quit);
-                        if (!ok) break;
-                        gdntc::fence_after_sync();
+                    const int slot = g & 1;
+                    ok = ok && wait(saddr(&c.p_full[slot]), (g >> 1) & 1, quit);
+                    if (!ok) break;
+                    gdntc::fence_after_sync();
 #pragma unroll
-                        for (int i = 0; i < kN / 16; ++i)
-                            gdntc::mma_bf16_ts(tmem + w * D, tmem + kSCol + slot * kN + i * 8,
-                                               gdntc::smem_desc_sw128_mn(v + i * 2048, kN * 128), kIdO, j > 0 || i > 0);
-                        gdntc::mma_commit(saddr(&c.pv_done[slot]));
-                        if (w == W - 1) gdntc::mma_commit(saddr(&c.v_empty[stage]));
-                    }
+                    for (int i = 0; i < kN / 16; ++i)
+                        gdntc::mma_bf16_ts(tmem, tmem + kSCol + slot * kN + i * 8, gdntc::smem_desc_sw128_mn(v + i * 2048, kN * 128),
+                                           kIdO, j > 0 || i > 0);
+                    gdntc::mma_commit(saddr(&c.pv_done[slot]));
+                    if (P == 2) gdntc::mma_commit_pair(saddr(&c.v_empty[stage]));
+                    else gdntc::mma_commit(saddr(&c.v_empty[stage]));
                 }
             }
             gdntc::mma_commit(saddr(&c.drain[1]));
@@ -414,86 +419,72 @@ attend(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtens
         }
         __syncwarp();
     } else {
-        const int w = warp / 4, row_in_tile = tid - w * 128;
-        const unsigned lane_addr = (unsigned)(warp & 3) << 21;  // 32 lanes each, in bits 16 and up
+        const unsigned lane_addr = (unsigned)warp << 21;  // 32 lanes each, in bits 16 and up
         const Buf bq{a.q, (size_t)a.batch * a.n_tok * a.h_q * D * 2}, bout{a.out, (size_t)a.batch * a.n_tok * a.h_q * D * 2},
             bpar{a.parent, (size_t)a.batch * (a.n_tok + 1) * 4};
-        constexpr int kBatch = W == 2 ? 1 : S::kChunks;  // column chunks of Q loaded at once: as the registers allow
         const float scale = a.scale_log2;
-        // With one M tile the scores of tile g are issued before the sums of g - 1,
-        // so a tile's scores only tell that the sums of g - 2 are done: a barrier
-        // for each S buffer keeps its phases apart.
-        auto sums_done = [&](int tile) {
-            return wait(saddr(&c.pv_done[W == 2 ? w : tile & 1]), W == 2 ? tile & 1 : (tile >> 1) & 1, quit);
-        };
+        // The scores of tile g are issued before the sums of g - 1, so a tile's scores
+        // only tell that the sums of g - 2 are done: a barrier for each S buffer
+        // keeps its phases apart.
+        auto sums_done = [&](int tile) { return wait(saddr(&c.pv_done[tile & 1]), (tile >> 1) & 1, quit); };
         int g = 0;
         unsigned seg = 0;
         bool ok = true;
         while (work.left > 0 && ok) {
             const bool first_segment = seg == 0;
             const Segment s = next_segment<kN>(a, plan, work);
-            const int kv = quotient(s.unit, plan.by_m_groups), row0 = ((s.unit - kv * plan.m_groups) * W + w) * kM, row = row0 + row_in_tile;
+            const int kv = quotient(s.unit, plan.by_m_groups), row0 = ((s.unit - kv * plan.m_groups) * P + rank) * kM, row = row0 + tid;
             const int ctx = s.slots - a.n_tok;
             // the M tile's queries: a warp's 32 rows, eight lanes to 128 bytes of a
             // row; the scores of the segment before have been read, so their
             // products are done with them
-            const bool live = row < rows, warp_live = row0 + (warp & 3) * 32 < rows;
+            const bool live = row < rows, warp_live = row0 + warp * 32 < rows;
             auto row_at = [&](int r) { return row_offset(a, plan, s.b, kv, r) * D; };
             const size_t q_row = live ? row_at(row) : 0;
             const uint4 *from[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const int r = row0 + (warp & 3) * 32 + i * 4 + lane / 8;
+                const int r = row0 + warp * 32 + i * 4 + lane / 8;
                 from[i] = r < rows ? reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q) + row_at(r)) + lane % 8
                                    : nullptr;
             }
+            uint4 x[S::kChunks][8];
 #pragma unroll
-            for (int k0 = 0; k0 < S::kChunks; k0 += kBatch) {
-                uint4 x[kBatch][8];
+            for (int k = 0; k < S::kChunks; ++k)
 #pragma unroll
-                for (int k = 0; k < kBatch; ++k)
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        x[k][i] = make_uint4(0, 0, 0, 0);
-                        if (from[i] && GDN_IN(from[i] + (k0 + k) * 8, 16, bq, st)) x[k][i] = from[i][(k0 + k) * 8];
-                    }
-#pragma unroll
-                for (int k = 0; k < kBatch; ++k) {
-                    // rows of 128 bytes, 16-byte units swizzled: in shared memory as the
-                    // descriptors want them, or on the way to tensor memory
-                    char *to = S::kQInTmem ? base + (pass_s - q_s) + warp * 4096
-                                           : base + w * S::kQBytes + (k0 + k) * (kM * 128) + (warp & 3) * 4096;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int r = i * 4 + lane / 8;
-                        *reinterpret_cast<uint4 *>(to + r * 128 + (lane % 8 ^ r % 8) * 16) = x[k][i];
-                    }
-                    if constexpr (S::kQInTmem) {
-                        __syncwarp();
-                        unsigned y[32];
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const uint4 u = *reinterpret_cast<const uint4 *>(to + lane * 128 + (i ^ lane % 8) * 16);
-                            y[4 * i] = u.x, y[4 * i + 1] = u.y, y[4 * i + 2] = u.z, y[4 * i + 3] = u.w;
-                        }
-                        gdntc::tmem_st32(tmem + lane_addr + kQCol + w * (D / 2) + (k0 + k) * 32, y);
-                        __syncwarp();
-                    }
+                for (int i = 0; i < 8; ++i) {
+                    x[k][i] = make_uint4(0, 0, 0, 0);
+                    if (from[i] && GDN_IN(from[i] + k * 8, 16, bq, st)) x[k][i] = from[i][k * 8];
                 }
+            // by way of shared memory (rows of 128 bytes, 16-byte units swizzled): a
+            // thread's own row, far from its neighbour's, would be 32 lines a load
+            char *pass = base + (pass_s - k_s) + warp * 4096;
+#pragma unroll
+            for (int k = 0; k < S::kChunks; ++k) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int r = i * 4 + lane / 8;
+                    *reinterpret_cast<uint4 *>(pass + r * 128 + (lane % 8 ^ r % 8) * 16) = x[k][i];
+                }
+                __syncwarp();
+                unsigned y[32];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const uint4 u = *reinterpret_cast<const uint4 *>(pass + lane * 128 + (i ^ lane % 8) * 16);
+                    y[4 * i] = u.x, y[4 * i + 1] = u.y, y[4 * i + 2] = u.z, y[4 * i + 3] = u.w;
+                }
+                gdntc::tmem_st32(tmem + lane_addr + kQCol + k * 32, y);
+                __syncwarp();
             }
-            if constexpr (S::kQInTmem) {
-                gdntc::tmem_wait_st();
-                gdntc::fence_before_sync();
-            } else {
-                gdntc::fence_smem_to_async();
-            }
-            if (w == 0 && row_in_tile == 0) c.odd_nodes[(seg + 1) & 3] = 0;
+            gdntc::tmem_wait_st();
+            gdntc::fence_before_sync();
+            if (tid == 0) c.odd_nodes[(seg + 1) & 3] = 0;
             __syncwarp();
             if (lane == 0) bar_arrive(saddr(&c.q_full));
             if (work.left > 0) {  // the next segment's queries on their way to L2
                 Work peek = work;
                 const Segment n = next_segment<kN>(a, plan, peek);
-                const int nkv = quotient(n.unit, plan.by_m_groups), r = ((n.unit - nkv * plan.m_groups) * W + w) * kM + row_in_tile;
+                const int nkv = quotient(n.unit, plan.by_m_groups), r = ((n.unit - nkv * plan.m_groups) * P + rank) * kM + tid;
                 if (r < rows)
                     gdndev::prefetch_l2_range(static_cast<const __nv_bfloat16 *>(a.q) + row_offset(a, plan, n.b, nkv, r) * D, D * 2, 0, 1);
             }
@@ -518,10 +509,10 @@ attend(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtens
             float m = -INFINITY;
             float2 sum = make_float2(0.f, 0.f);
             for (int j = 0; j < s.n; ++j, ++g) {
-                const int slot = W == 2 ? w : g & 1, tile = s.tile0 + j;
+                const int slot = g & 1, tile = s.tile0 + j;
                 const bool edge = (tile + 1) * kN > ctx;
-                ok = wait(saddr(&c.s_full[slot]), W == 2 ? g & 1 : (g >> 1) & 1, quit);
-                if (edge && w == 0) ok = ok && wait(saddr(&c.v_full[g % kStages]), (g / kStages) & 1, quit);
+                ok = wait(saddr(&c.s_full[slot]), (g >> 1) & 1, quit);
+                if (edge) ok = ok && wait(saddr(&c.v_full[g % kStages]), (g / kStages) & 1, quit);
                 ok = __all_sync(~0u, ok);
                 if (!ok) break;
                 gdntc::fence_after_sync();
@@ -562,11 +553,11 @@ attend(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtens
 #pragma unroll 1
                             for (int k = 0; k < D; k += 32) {
                                 unsigned o[32];
-                                gdntc::tmem_ld32(tmem + lane_addr + w * D + k, o);
+                                gdntc::tmem_ld32(tmem + lane_addr + k, o);
                                 gdntc::tmem_wait_ld();
 #pragma unroll
                                 for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                                gdntc::tmem_st32(tmem + lane_addr + w * D + k, o);
+                                gdntc::tmem_st32(tmem + lane_addr + k, o);
                             }
                             if (far) m = top;
                             sum.x *= f;
@@ -593,13 +584,13 @@ attend(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtens
                     sum = add2(sum, add2(add2(part[0], part[1]), add2(part[2], part[3])));
                     gdntc::tmem_wait_st();
                 }
-                if (edge && w == 0) {
+                if (edge) {
                     // v past the last slot becomes zeros, and so does what is no number
                     // among the drafted nodes' values: 0 x NaN must not reach the rows
                     // that do not see them; those that do get it back at the end
-                    char *v = base + (v_s - q_s) + (g % kStages) * S::kTileBytes;
+                    char *v = base + (v_s - k_s) + (g % kStages) * S::kTileBytes;
                     const int lo = max(0, ctx - tile * kN);
-                    for (int i = row_in_tile; i < (kN - lo) * S::kChunks * 8; i += 128) {
+                    for (int i = tid; i < (kN - lo) * S::kChunks * 8; i += 128) {
                         const int r = lo + i / (S::kChunks * 8), u = i % (S::kChunks * 8);
                         uint4 *p = reinterpret_cast<uint4 *>(v + (u / 8) * (kN * 128) + r * 128 + (u % 8) * 16);
                         const int node = tile * kN + r - ctx;
@@ -636,19 +627,19 @@ attend(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtens
                 const bool whole = s.n == s.tiles;
                 const float total = sum.x + sum.y, inv = whole ? 1.f / total : 1.f;
                 const unsigned long long odd = *(volatile unsigned long long *)&c.odd_nodes[seg & 3] & path;
-                const size_t piece = 2 * blockIdx.x + (first_segment ? 0 : 1);
-                const int pr = w * kM + row_in_tile;
-                const Buf bo{pieces.o, (size_t)2 * gridDim.x * W * kM * D * 4}, bms{pieces.ms, (size_t)2 * gridDim.x * W * kM * 8};
-                if (!whole && row_in_tile == 0 && w == 0) pieces.unit[piece] = s.b * plan.units + s.unit;
+                const size_t piece = 2 * cluster + (first_segment ? 0 : 1);
+                const int pr = rank * kM + tid;
+                const Buf bo{pieces.o, (size_t)2 * plan.blocks * P * kM * D * 4}, bms{pieces.ms, (size_t)2 * plan.blocks * P * kM * 8};
+                if (!whole && tid == 0 && rank == 0) pieces.unit[piece] = s.b * plan.units + s.unit;
                 if (!whole && live) {
-                    float2 *f = pieces.ms + piece * (W * kM) + pr;
+                    float2 *f = pieces.ms + piece * (P * kM) + pr;
                     if (GDN_IN(f, 8, bms, st)) *f = make_float2(m == -INFINITY ? m : m * scale, total);
                 }
 #pragma unroll 1
                 for (int k = 0; k < D; k += 32) {
                     unsigned o[32];
                     __syncwarp();
-                    gdntc::tmem_ld32(tmem + lane_addr + w * D + k, o);
+                    gdntc::tmem_ld32(tmem + lane_addr + k, o);
                     gdntc::tmem_wait_ld();
                     if (!live) continue;
                     float f[32];
@@ -681,11 +672,11 @@ attend(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtens
                                     make_uint4(pack_bf16(f[i], f[i + 1]), pack_bf16(f[i + 2], f[i + 3]),
                                                pack_bf16(f[i + 4], f[i + 5]), pack_bf16(f[i + 6], f[i + 7]));
                     } else {
-                        float4 *to = pieces.o + (piece * (D / 4) + k / 4) * (W * kM) + pr;
+                        float4 *to = pieces.o + (piece * (D / 4) + k / 4) * (P * kM) + pr;
 #pragma unroll
                         for (int i = 0; i < 8; ++i)
-                            if (GDN_IN(to + i * (W * kM), 16, bo, st))
-                                to[i * (W * kM)] = make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
+                            if (GDN_IN(to + i * (P * kM), 16, bo, st))
+                                to[i * (P * kM)] = make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
                     }
                 }
             }
@@ -704,6 +695,7 @@ attend(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtens
                 if (GDN_IN(to + i, 16, bout, st)) to[i] = make_uint4(0, 0, 0, 0);
         }
     __syncthreads();
+    if (P == 2) cluster_sync();  // the other block may still load into this one's shared memory
     if (c.quit && tid == 0 && st) atomicOr(st, GDN_DEV_SCHED);
     if (warp == kScoreWarp) {
         gdntc::fence_after_sync();
@@ -720,11 +712,11 @@ attend(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtens
 // beginning of block `index`, if that is its first cut.
 constexpr int kJoinWarps = 4;
 
-template <int D, int W>
+template <int D, int P>
 __global__ void __launch_bounds__(kJoinWarps * 32, 8)
 join_pieces(const __grid_constant__ AttnArgs a, const __grid_constant__ Plan plan, const __grid_constant__ Pieces pieces,
             int share, int items, int chunks, bool by_unit) {
-    constexpr int kRows = W * kM, kCols = D / 8, kAhead = 4;
+    constexpr int kRows = P * kM, kCols = D / 8, kAhead = 4;
     __shared__ float4 part[kJoinWarps][2][32];
     __shared__ float top[kJoinWarps][32], total[kJoinWarps][32];
     __shared__ unsigned short list[kJoinWarps][2 * kMaxBlocks];
@@ -859,40 +851,40 @@ int block_count() {
     return sms <= 0 ? 152 : sms < kMaxBlocks ? sms : kMaxBlocks;
 }
 
-int m_tiles(const attn_dims *d, int n_tok) {
-    return d->d_head < 256 && n_tok * (d->h_q / d->h_kv) > kM ? 2 : 1;
-}
+// Blocks of a cluster: two where there is more than one M tile.
+int pair(const attn_dims *d, int n_tok) { return n_tok * (d->h_q / d->h_kv) > kM ? 2 : 1; }
 
-template <int D, int W>
+template <int D, int P>
 int launch(const attn_dims *d, const AttnArgs &a, void *ws, cudaStream_t st) {
-    using S = Shape<D, W>;
+    using S = Shape<D>;
     static bool set[256] = {};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 256) return GDN_ERR_CUDA;
     if (!set[dev]) {
-        if (cudaFuncSetAttribute(attend<D, W>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kSmem) != cudaSuccess)
+        if (cudaFuncSetAttribute(attend<D, P>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kSmem) != cudaSuccess)
             return GDN_ERR_CUDA;
         set[dev] = true;
     }
     CUtensorMap k_map, v_map;
-    if (!pool_map(&k_map, d, a.k_pages, S::kN) || !pool_map(&v_map, d, a.v_pages, S::kN)) return GDN_ERR_CUDA;
-    const int blocks = block_count();
+    if (!pool_map(&k_map, d, a.k_pages, S::kN / P) || !pool_map(&v_map, d, a.v_pages, S::kN / P)) return GDN_ERR_CUDA;
+    const int blocks = block_count() / P;
     char *at = static_cast<char *>(ws);
-    const size_t rows_of_pieces = (size_t)2 * blocks * W * kM;
+    const size_t rows_of_pieces = (size_t)2 * blocks * P * kM;
     const Pieces pieces{reinterpret_cast<float4 *>(at), reinterpret_cast<float2 *>(at + rows_of_pieces * D * 4),
                         reinterpret_cast<int *>(at + rows_of_pieces * (D * 4 + 8))};
-    const int group = a.h_q / a.h_kv, rows = a.n_tok * group, m_groups = (rows + W * kM - 1) / (W * kM);
+    const int group = a.h_q / a.h_kv, rows = a.n_tok * group, m_groups = (rows + P * kM - 1) / (P * kM);
     auto by = [](int n) { return (unsigned)(((1ull << 32) + n - 1) / n); };
     const Plan plan{group, rows, m_groups, a.h_kv * m_groups, blocks, by(group), by(m_groups), by(blocks)};
-    if (gdndev::launch_pdl(attend<D, W>, dim3(blocks), dim3(S::kThreads), S::kSmem, st, k_map, v_map, a, plan, pieces) != cudaSuccess)
+    if (gdndev::launch_pdl_clusters(attend<D, P>, P, dim3(blocks * P), dim3(S::kThreads), S::kSmem, st, k_map, v_map, a, plan, pieces) !=
+        cudaSuccess)
         return GDN_ERR_CUDA;
     // a unit has about blocks / units pieces, and one more
     const int64_t units = (int64_t)a.batch * plan.units;
     const bool by_unit = units < blocks;
     const int indexes = by_unit ? (int)units : blocks, per_unit = blocks / indexes + 1;
     const int share = per_unit <= 4 ? 1 : per_unit <= 8 ? 2 : 4;
-    const int chunks = ((rows < W * kM ? rows : W * kM) + 31) / 32, items = indexes * chunks * (D / 8);
-    return gdndev::launch_pdl(join_pieces<D, W>, dim3((items * share + kJoinWarps - 1) / kJoinWarps), dim3(kJoinWarps * 32), 0, st, a, plan, pieces, share, items,
+    const int chunks = ((rows < P * kM ? rows : P * kM) + 31) / 32, items = indexes * chunks * (D / 8);
+    return gdndev::launch_pdl(join_pieces<D, P>, dim3((items * share + kJoinWarps - 1) / kJoinWarps), dim3(kJoinWarps * 32), 0, st, a, plan, pieces, share, items,
                               chunks, by_unit) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
@@ -901,13 +893,14 @@ int launch(const attn_dims *d, const AttnArgs &a, void *ws, cudaStream_t st) {
 namespace gdnattn {
 
 size_t tc_workspace(const attn_dims *d, int n_tok) {
-    return (size_t)2 * block_count() * (m_tiles(d, n_tok) * kM * (d->d_head * 4 + 8) + 4);
+    const size_t p = pair(d, n_tok), blocks = block_count() / p;
+    return 2 * blocks * (p * kM * (d->d_head * 4 + 8) + 4);
 }
 
 int tc_launch(const attn_dims *d, const AttnArgs &a, void *ws, cudaStream_t st) {
-    if (a.d == 256) return launch<256, 1>(d, a, ws, st);
-    if (m_tiles(d, a.n_tok) == 2) return a.d == 64 ? launch<64, 2>(d, a, ws, st) : launch<128, 2>(d, a, ws, st);
-    return a.d == 64 ? launch<64, 1>(d, a, ws, st) : launch<128, 1>(d, a, ws, st);
+    if (pair(d, a.n_tok) == 2)
+        return a.d == 64 ? launch<64, 2>(d, a, ws, st) : a.d == 128 ? launch<128, 2>(d, a, ws, st) : launch<256, 2>(d, a, ws, st);
+    return a.d == 64 ? launch<64, 1>(d, a, ws, st) : a.d == 128 ? launch<128, 1>(d, a, ws, st) : launch<256, 1>(d, a, ws, st);
 }
 
 }  // namespace gdnattn
