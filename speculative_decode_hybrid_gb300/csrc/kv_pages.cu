@@ -4,8 +4,12 @@
 // PR #626, What Changed: the committed context's KV beside the recurrent
 // state.)
 //
-// All three are bound by latency at a few requests and by the bytes of the
-// moved rows at many. A page is free while its reference count is 0 and the
+// All are bound by latency: a chain of lookups (lengths, parents, table entries)
+// stands before the first moved byte. Commit of 16 requests' paths of 11 in 16
+// layers of 8 heads of 128 bf16 (23 MB moved) 7.5 us, with slices and rows found
+// by multiplications and 64 registers (13 us with divisions); a fork's copy of 16
+// tails in 8 layers (13 MB) 6 us; the one-block kernels that take and give back
+// pages 3 to 8 us, five dependent reads long. A page is free while its reference count is 0 and the
 // lowest free id is taken first, so that the counts are the only state of the
 // pool and integer atomics, in whatever order, give the same result.
 #include <cuda_runtime.h>

@@ -13,8 +13,7 @@
 // u (1 - sum of the removed p) < p(x). A node's index exceeds its parent's:
 // one pass over the nodes in index order, with the last accepted node in hand,
 // is the walk. The next token is the largest r_v / noise_v: an argmax, which
-// needs neither a prefix sum nor r's normalisation, and whose result does not
-// depend on the order of any sum.
+// needs neither a prefix sum nor r's normalisation.
 //
 // Two launches. sample_rows reads the logits once (all N rows: each drafted
 // token's probability is an output), every block an equal, contiguous part of
@@ -24,7 +23,11 @@
 // all of them repeat the walk, then each takes a slice of the accepted row (and
 // of q and the noise), and the first joins their candidates; what does not
 // depend on the sums is read while they are still being taken. The first launch
-// is bound by the logits' bytes, the second by latency.
+// is bound by the logits' bytes (38 us for 224 MB, 0.87 of the measured copy rate),
+// the second by latency: 14 us for the same 16 requests, in which a row's loads
+// follow the walk, the walk the statistics, and those the tokens. Its blocks are
+// held to 64 registers: at one block an SM, only 15 of the 16 clusters of eight
+// fit the GPU at once (47 us).
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
