@@ -452,8 +452,9 @@ size_t spec_topk_workspace_bytes(int32_t rows, int32_t k);
  * and is never written (GDN_DEV_PAGE).
  *
  *   batch        B >= 1 requests, B <= 65535
- *   layers       Y >= 1 layers of the kv_* calls' caches [Y][n_pages]...;
- *                the attn_* calls work on one layer and ignore it
+ *   layers       Y >= 1 layers of the kv_* calls' caches [Y][n_pages]...
+ *                (Y * h_kv * h_kv < 2^31 there, Y <= 65535); the attn_* calls
+ *                work on one layer and ignore it
  *   h_q, h_kv    query and key/value heads, h_q % h_kv == 0, query head h
  *                reads key/value head floor(h * h_kv / h_q); at most 1024
  *   d_head       64, 128 or 256

@@ -48,6 +48,9 @@ struct Slices {
     }
 };
 
+// Whether quotient() is exact for every slice.
+bool slices_fit(const attn_dims *d) { return 2ll * d->layers * d->h_kv * d->h_kv < (1ll << 32); }
+
 Slices slices_of(const attn_dims *d, void *k, void *v) {
     const size_t head = (size_t)d->page_tokens * d->d_head * gdnhost::attn_elem_bytes(d) / 16;
     return {static_cast<uint4 *>(k), static_cast<uint4 *>(v), d->layers, d->h_kv, reciprocal(d->h_kv),
@@ -445,7 +448,7 @@ extern "C" int kv_commit_path(const attn_dims *dims, int32_t n_nodes, const int3
                               void *k_pages, void *v_pages, int32_t *ctx_out, int32_t *dev_status,
                               gdn_stream_t stream) {
     if (const int rc = gdnhost::check_attn(dims)) return rc;
-    if (n_nodes < 2 || n_nodes > kMaxNodes) return GDN_ERR_DIMS;
+    if (n_nodes < 2 || n_nodes > kMaxNodes || !slices_fit(dims)) return GDN_ERR_DIMS;
     if (!accept_node || !ctx_len || !ctx_out || (parent_dev && (!page_table || !k_pages || !v_pages))) return GDN_ERR_NULL;
     using gdnhost::aligned_to;
     if (!aligned_to(k_pages, 16) || !aligned_to(v_pages, 16)) return GDN_ERR_ALIGN;
@@ -494,7 +497,7 @@ extern "C" int kv_pages_fork(const attn_dims *dims, int32_t n_fork, const int32_
                              int32_t *page_table, int32_t *ctx_len, int32_t *page_ref, void *k_pages, void *v_pages,
                              void *workspace, size_t workspace_bytes, int32_t *dev_status, gdn_stream_t stream) {
     if (const int rc = gdnhost::check_attn(dims)) return rc;
-    if (n_fork < 1 || n_fork > dims->batch) return GDN_ERR_DIMS;
+    if (n_fork < 1 || n_fork > dims->batch || !slices_fit(dims)) return GDN_ERR_DIMS;
     if (!k_pages || !v_pages) return GDN_ERR_NULL;
     if (const int rc = check_pages(dims, {src, dst, page_table, ctx_len, page_ref}, workspace, workspace_bytes, dev_status))
         return rc;

@@ -140,6 +140,8 @@ def test_commit_and_pages_refuse(lib):
     d = dims()
     for n in (0, 1, 66):
         assert commit(lib, d, n_nodes=n) == G.GDN_ERR_DIMS
+    many = dims(layers=2048, h_q=1024, h_kv=1024)
+    assert commit(lib, many) == G.GDN_ERR_DIMS and fork(lib, many) == G.GDN_ERR_DIMS
     for name in ("node", "ctx", "table", "k", "v", "out"):
         assert commit(lib, d, **{name: None}) == G.GDN_ERR_NULL, name
     for name in ("k", "v"):
