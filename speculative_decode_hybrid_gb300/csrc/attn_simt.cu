@@ -2,14 +2,17 @@
 // throughout (attn_verify_span / attn_tree_verify with GDN_F32).
 //
 // One pass over the keys with the running maximum and sum of each row's
-// softmax. A block takes 8 R query rows (nodes x query heads of one key/value
-// head) and a part of the slots; a warp takes R of the rows, a lane one of a
-// tile's 32 slots for the scores and D / 32 of the columns for the sums. The
-// next tile is copied into shared memory while one is worked on. R is 1, 2, 4 or
-// 8: the least that takes all rows in one block, so that a single token's few
-// heads do not carry empty rows along. Parts are joined by a second kernel.
-// Bound by the f32 pipe and the shared-memory reads that feed it (4 D operations
-// per row and slot) with many rows, by the copies with few.
+// softmax. A row is a node's query head of one key/value head.
+//
+// Few rows (attend(): single tokens, short chains): a block takes 8 R rows and a
+// part of the slots; a warp takes R of the rows, a lane one of a tile's 32 slots
+// for the scores and D / 32 of the columns for the sums. The next tile is copied
+// into shared memory while one is worked on. R is 1, 2 or 4: the least that takes
+// all rows in one block, so that a single token's few heads do not carry empty
+// rows along. Bound by the copies' latency: 8 requests' single tokens, 16 heads of
+// 128 over 2,000 slots take 20.6 us with the join (the bytes alone 4.1).
+//
+// Many rows: attend_many(), below. Parts are joined by a second kernel.
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -191,6 +194,16 @@ __global__ void __launch_bounds__(kThreads) attend(AttnArgs a, int parts, float 
 // warps are `row_warps` by kWarps / row_warps: those in a row of warps share a tile,
 // the others have tiles, and partial results, of their own. The next tile's keys
 // are copied while the weights multiply the values, its values during the scores.
+// Bound by the f32 pipe (4 D operations per row and slot) and by the shared-memory
+// reads that feed it: a lane reads 48 numbers for 128 products of the scores (at
+// 32 lanes' numbers a cycle that is 2/3 of the pipe's rate) and 24 for 128 of the
+// sums. Measured, with a warp of R rows and a slot a lane for comparison:
+// 8 requests, 64 nodes, 32 heads of 128 over 4,000 slots 704 us (1,217; the pipe
+// alone 417); 4 spans of 16, 32 heads of 128 over 4,000 131 us (196; 52); 22 nodes,
+// 16 heads of 256 over 8,000 115 us (183; 36); 8 trees of 40, 8 heads of 64 over
+// 3,000 107 us (113; 24: 40 rows fill 64). Pairs of f32 products in one
+// instruction in the sums took 8 % off; in the scores, whose reads bound them,
+// nothing, nor did a rescaling left out where no maximum moved.
 constexpr int kLaneSlots = 4;
 
 template <int D, int R>
@@ -285,16 +298,17 @@ attend_many(AttnArgs a, int parts, int row_warps_log, float *part_o, float2 *par
     const float *kw = ks + (slot_warp * kTile + e) * M::kKRow, *vw = vs + slot_warp * kTile * D + e * 4,
                 *qw = qs + (row_warp * M::kRows + g) * M::kKRow;
     float *pw = ps + warp * kTile * M::kPRow + g * R;
-    float m[R], l[R], o[R][kChunks * 4];
+    float m[R], l[R];
+    float2 o[R][kChunks * 2];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
         m[r] = -INFINITY, l[r] = 0.f;
 #pragma unroll
-        for (int c = 0; c < kChunks * 4; ++c) o[r][c] = 0.f;
+        for (int c = 0; c < kChunks * 2; ++c) o[r][c] = make_float2(0.f, 0.f);
     }
     // the sums take a tile's weights; with `edge` a weight below zero is no part of them, whatever v holds
     auto add = [&](auto edge) {
-#pragma unroll 1
+#pragma unroll 2
         for (int j = 0; j < kTile; ++j) {
             float p[R];
             float4 v[kChunks];
@@ -308,10 +322,9 @@ attend_many(AttnArgs a, int parts, int row_warps_log, float *part_o, float2 *par
                 if (!decltype(edge)::value || p[r] >= 0.f || p[r] != p[r])
 #pragma unroll
                     for (int c = 0; c < kChunks; ++c) {
-                        o[r][c * 4] = fmaf(p[r], v[c].x, o[r][c * 4]);
-                        o[r][c * 4 + 1] = fmaf(p[r], v[c].y, o[r][c * 4 + 1]);
-                        o[r][c * 4 + 2] = fmaf(p[r], v[c].z, o[r][c * 4 + 2]);
-                        o[r][c * 4 + 3] = fmaf(p[r], v[c].w, o[r][c * 4 + 3]);
+                        const float2 pp = make_float2(p[r], p[r]);
+                        o[r][c * 2] = gdndev::fma2(pp, make_float2(v[c].x, v[c].y), o[r][c * 2]);
+                        o[r][c * 2 + 1] = gdndev::fma2(pp, make_float2(v[c].z, v[c].w), o[r][c * 2 + 1]);
                     }
         }
     };
@@ -374,7 +387,7 @@ attend_many(AttnArgs a, int parts, int row_warps_log, float *part_o, float2 *par
                     sc[r][j] = seen >> (4 * r + j) & 1 ? p : -1.f;
                 }
 #pragma unroll
-                for (int c = 0; c < kChunks * 4; ++c) o[r][c] *= scale;
+                for (int c = 0; c < kChunks * 2; ++c) o[r][c] = gdndev::mul2(o[r][c], make_float2(scale, scale));
             }
 #pragma unroll
             for (int j = 0; j < kJ; ++j)
@@ -409,7 +422,7 @@ attend_many(AttnArgs a, int parts, int row_warps_log, float *part_o, float2 *par
             for (int c = 0; c < kChunks; ++c) {
                 float *to = part_o + at * D + e * 4 + c * 32;
                 if (GDN_IN(to, 16, bo, st))
-                    *reinterpret_cast<float4 *>(to) = make_float4(o[r][c * 4], o[r][c * 4 + 1], o[r][c * 4 + 2], o[r][c * 4 + 3]);
+                    *reinterpret_cast<float4 *>(to) = make_float4(o[r][c * 2].x, o[r][c * 2].y, o[r][c * 2 + 1].x, o[r][c * 2 + 1].y);
             }
         }
     }
