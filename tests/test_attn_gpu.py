@@ -229,6 +229,44 @@ def test_attention_leaves_out_lengths_and_flags_pages(dtype):
     assert np.all(np.abs(f64(out[1]) - want) <= R.attention_bound(want, mass, big, d, 44, dtype == "bf16"))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("T,h_q,h_kv,n", [(17, 3, 3, 2900), (8, 4, 1, 3000), (25, 8, 2, 2111), (16, 8, 1, 1500), (64, 24, 3, 700)])
+def test_attention_many_rows_over_long_contexts(dtype, d, T, h_q, h_kv, n):
+    """17 to 512 rows of a key/value head, each over many tiles, their maximum
+    rising along the slots, beside a request that has hardly any."""
+    g = np.random.default_rng(T * d + n)
+    cache, q, parents = make(g, [n, 1, 333], T, h_q, h_kv, d, 16, dtype, True)
+    k, v = cache.rows(0, np.arange(n + T))
+    cache.put(0, np.arange(n + T), k.float() * torch.linspace(0.2, 4.0, n + T, device="cuda")[:, None, None], v)
+    out, st = attend(cache, q, parents, d ** -0.5)
+    check(cache, q, parents, out, d ** -0.5)
+    assert int(st.item()) == 0
+    again, _ = attend(cache, q, parents, d ** -0.5)
+    assert torch.equal(out, again)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 256])
+def test_attention_many_rows_leave_out_lengths_and_flag_pages(dtype, d):
+    g = np.random.default_rng(15)
+    T, n = 20, 300
+    cache, q, _ = make(g, [n, n, n], T, 16, 2, d, 16, dtype, False)
+    cache.ctx_dev[1] = cache.width * 16 - T + 1
+    out, st = attend(cache, q, None, d ** -0.5)
+    check(cache, q, None, out, d ** -0.5, skip=(1,))
+    assert torch.count_nonzero(out[1]).item() == 0 and int(st.item()) == G.GDN_DEV_LENGTH
+    cache.ctx_dev[1] = n
+    cache.table_dev[1, 9], cache.table_dev[1, 19] = cache.n_pages, -3   # 19: the last page, where drafted nodes lie
+    out, st = attend(cache, q, None, d ** -0.5)
+    assert int(st.item()) == G.GDN_DEV_PAGE
+    k, v = (f64(x) for x in cache.rows(1, np.arange(n + T)))
+    for j in (9, 19):
+        k[j * 16:j * 16 + 16], v[j * 16:j * 16 + 16] = 0, 0
+    want, mass, big = R.attention(f64(q[1]), k, v, R.chain(T + 1), n, d ** -0.5)
+    assert np.all(np.abs(f64(out[1]) - want) <= R.attention_bound(want, mass, big, d, n + T, dtype == "bf16"))
+
+
 def test_attention_device_parent_is_checked_again():
     g = np.random.default_rng(6)
     cache, q, parents = make(g, [70], 6, 4, 2, 64, 16, "bf16", True)
