@@ -4,15 +4,8 @@
 // One pass over the keys with the running maximum and sum of each row's
 // softmax. A row is a node's query head of one key/value head.
 //
-// Few rows (attend(): single tokens, short chains): a block takes 8 R rows and a
-// part of the slots; a warp takes R of the rows, a lane one of a tile's 32 slots
-// for the scores and D / 32 of the columns for the sums. The next tile is copied
-// into shared memory while one is worked on. R is 1, 2 or 4: the least that takes
-// all rows in one block, so that a single token's few heads do not carry empty
-// rows along. Bound by the copies' latency: 8 requests' single tokens, 16 heads of
-// 128 over 2,000 slots take 20.6 us with the join (the bytes alone 4.1).
-//
-// Many rows: attend_many(), below. Parts are joined by a second kernel.
+// Few rows (single tokens, short chains): attend(). Many rows: attend_many(). Parts
+// of a request's slots are joined by a second kernel.
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -33,32 +26,64 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kTile = 32;
 constexpr int kMaxParts = 128;
 
+// Few rows: R of them a block, each warp with slots of its own, U at a time (2 U
+// where half a warp spans a head). A lane holds its columns of the queries, keys,
+// values and sums in registers; the next keys are asked for once the products with
+// the last are made, the next values once the sums are. Nothing but weights goes
+// through shared memory, whose reads bound a form with shared tiles (in brackets):
+// 4 requests' single tokens, 16 heads of 256 over 5,000 slots 41 us (100; the bytes
+// alone 21); 8 requests', 16 heads of 128 over 2,000 15.3 us with the join (20.6;
+// 4.1); one over 777 10.8 us (14.7), two launches. Bound by the wait for the loads,
+// 64 KB of them in flight on an SM, and by about as many operations for the sums
+// over lanes as for the products.
 template <int D, int R>
-struct Shared {
-    float q[kWarps * R][D];
-    float k[2][kTile][D + 4];  // rows 16 bytes apart in the banks
-    float v[2][kTile][D];
-    float p[kWarps * R][kTile];
-    unsigned long long path[GDN_MAX_TOKENS];
-    int parent[GDN_MAX_TOKENS + 1];
+struct Few {
+    static constexpr int kLanes = D == 64 ? 16 : 32, kGroups = 32 / kLanes, kC = D / (4 * kLanes);
+    static constexpr int kU = D == 256 && R == 8 ? 4 : 8, kStep = kU * kGroups;  // slots a warp takes at a time
+    static constexpr int kScores = R * kU;                                       // of a group of lanes
+    static constexpr int kOwn = kScores >= kLanes ? kScores / kLanes : 1;        // of them a lane has in the end
+    static constexpr int kSame = kScores >= kLanes ? 1 : kLanes / kScores;       // lanes that have the same
+    struct Smem {
+        float o[kWarps][R][D];
+        float p[kWarps][kGroups][kScores];
+        float scale[kWarps][R], m[kWarps][R], l[kWarps][R];
+        unsigned long long path[GDN_MAX_TOKENS];
+        int parent[GDN_MAX_TOKENS + 1];
+    };
 };
 
-__device__ __forceinline__ void copy16(void *to, const void *from, bool there) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((unsigned)__cvta_generic_to_shared(to)), "l"(from),
-                 "r"(there ? 16 : 0)
-                 : "memory");  // zeros where there is nothing to copy
+// x[N] summed over `kLanes` lanes; lane i is left with the sums of its kOwn places
+// from i * N / kLanes on (N < kLanes: of place i * N / kLanes). Halves are exchanged,
+// so that N sums take N shuffles and not 5 N.
+template <int N, int kW>
+__device__ __forceinline__ void sum_apart(float *x, int lane) {
+    if constexpr (kW > 0) {
+        if constexpr (N > 1) {
+            const bool upper = lane & kW;
+#pragma unroll
+            for (int i = 0; i < N / 2; ++i) {
+                const float keep = upper ? x[i + N / 2] : x[i], send = upper ? x[i] : x[i + N / 2];
+                x[i] = keep + __shfl_xor_sync(~0u, send, kW);
+            }
+            sum_apart<N / 2, kW / 2>(x, lane);
+        } else {
+            x[0] += __shfl_xor_sync(~0u, x[0], kW);
+            sum_apart<1, kW / 2>(x, lane);
+        }
+    }
 }
 
 // grid (row blocks, B * h_kv, parts); partial results [B][n_tok][h_q][parts]
 // of D sums (relative to the maximum) and of (maximum, sum) in powers of two.
 template <int D, int R>
-__global__ void __launch_bounds__(kThreads) attend(AttnArgs a, int parts, float *part_o, float2 *part_ms) {
+__global__ void __launch_bounds__(kThreads, R == 8 || D == 256 ? 1 : 2) attend(AttnArgs a, int parts, float *part_o, float2 *part_ms) {
+    using F = Few<D, R>;
+    constexpr int kC = F::kC, kU = F::kU, kG = F::kGroups, kOwn = F::kOwn;
     extern __shared__ __align__(16) char raw[];
-    Shared<D, R> &s = *reinterpret_cast<Shared<D, R> *>(raw);
-    constexpr int kCols = D / 32, kRows = kWarps * R;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    typename F::Smem &s = *reinterpret_cast<typename F::Smem *>(raw);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, sub = lane % F::kLanes, grp = lane / F::kLanes;
     const int b = blockIdx.y / a.h_kv, kv = blockIdx.y % a.h_kv, part = blockIdx.z;
-    const int group = a.h_q / a.h_kv, rows = a.n_tok * group, row0 = blockIdx.x * kRows;
+    const int group = a.h_q / a.h_kv, rows = a.n_tok * group, row0 = blockIdx.x * R;
     int32_t *st = a.status;
     const size_t B = a.batch, pool = ((size_t)a.n_pages * a.h_kv << a.page_shift) * D * 4, heads = B * a.n_tok * a.h_q;
     const Buf bq{a.q, heads * D * 4}, bk{a.k_pages, pool}, bv{a.v_pages, pool}, bt{a.table, B * (size_t)a.width * 4},
@@ -67,125 +92,169 @@ __global__ void __launch_bounds__(kThreads) attend(AttnArgs a, int parts, float 
     gdndev::pdl_wait();
     const int slots = gdnattn::slots_of(a, b), ctx = slots - a.n_tok;
     if (slots == 0 && tid == 0 && st) atomicOr(st, GDN_DEV_LENGTH);
-    const int per = ((slots + parts - 1) / parts + kTile - 1) / kTile * kTile;
-    const int s0 = min(slots, part * per), s1 = min(slots, s0 + per);
+    constexpr int kBlock = kWarps * F::kStep;
+    const int per = ((slots + parts - 1) / parts + kBlock - 1) / kBlock * kBlock;
+    const int s0 = (int)min((long long)slots, (long long)part * per), s1 = (int)min((long long)slots, (long long)s0 + per);
     const float *kp = static_cast<const float *>(a.k_pages), *vp = static_cast<const float *>(a.v_pages);
-    // a warp copies four rows of a tile; their pages are looked up first
-    auto fetch = [&](int base, int buf) {
-#pragma unroll
-        for (int i = 0; i < kTile / kWarps; ++i) {
-            const int r = warp * (kTile / kWarps) + i, slot = base + r;
-            size_t at = 0;
-            bool there = false;
-            if (slot < s1) {
-                const int32_t *e = a.table + (size_t)b * a.width + (slot >> a.page_shift);
-                const int page = GDN_IN(e, 4, bt, st) ? *e : -1;
-                there = page >= 0 && page < a.n_pages;
-                if (!there && lane == 0 && st) atomicOr(st, GDN_DEV_PAGE);
-                at = ((((size_t)(there ? page : 0) * a.h_kv + kv) << a.page_shift) + (slot & ((1 << a.page_shift) - 1))) * D;
-            }
-#pragma unroll
-            for (int c = lane * 4; c < D; c += 128) {
-                copy16(&s.k[buf][r][c], kp + at + c, there && GDN_IN(kp + at + c, 16, bk, st));
-                copy16(&s.v[buf][r][c], vp + at + c, there && GDN_IN(vp + at + c, 16, bv, st));
-            }
-        }
-        asm volatile("cp.async.commit_group;" ::: "memory");
+    // lane i knows the page of the warp's i-th slot
+    auto page_of = [&](int base) {
+        const int slot = base + lane;
+        if (lane >= F::kStep || slot >= s1) return -2;  // nothing there
+        const int32_t *f = a.table + (size_t)b * a.width + (slot >> a.page_shift);
+        return GDN_IN(f, 4, bt, st) ? *f : -1;
     };
-    if (s0 < s1) fetch(s0, 0);
-    for (int i = tid; i < kRows * (D / 4); i += kThreads) {
-        const int r = i / (D / 4), c = i % (D / 4) * 4;
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (row0 + r < rows) {
-            const int t = (row0 + r) / group, h = kv * group + (row0 + r) % group;
-            const float *f = static_cast<const float *>(a.q) + (((size_t)b * a.n_tok + t) * a.h_q + h) * D + c;
-            if (GDN_IN(f, 16, bq, st)) x = gdndev::ld4(f);
+    auto place_of = [&](int base, int page) {
+        const int slot = base + lane;
+        if (page >= 0 && page < a.n_pages)
+            return (long long)((((size_t)page * a.h_kv + kv) << a.page_shift) + (slot & ((1 << a.page_shift) - 1))) * D;
+        if (page != -2 && st) atomicOr(st, GDN_DEV_PAGE);
+        return -1ll;
+    };
+    auto load = [&](float4 (&x)[kU][kC], const float *from, const Buf &bf, long long place) {
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+            const long long at = __shfl_sync(~0u, place, u * kG + grp);
+#pragma unroll
+            for (int c = 0; c < kC; ++c) {
+                const float *f = from + at + c * 128 + sub * 4;
+                x[u][c] = at >= 0 && GDN_IN(f, 16, bf, st) ? gdndev::ld4(f) : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
         }
-        *reinterpret_cast<float4 *>(&s.q[r][c]) = x;
+    };
+    float4 q[R][kC], o[R][kC], k[kU][kC], v[kU][kC];
+    int base = s0 + warp * F::kStep, next = page_of(base);
+    long long place = place_of(base, next);
+    next = page_of(base + kBlock);
+    load(k, kp, bk, place);
+    load(v, vp, bv, place);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const int t = (row0 + r) / group, h = kv * group + (row0 + r) % group;
+        const float *f = static_cast<const float *>(a.q) + (((size_t)b * a.n_tok + t) * a.h_q + h) * D + sub * 4;
+#pragma unroll
+        for (int c = 0; c < kC; ++c) {
+            q[r][c] = row0 + r < rows && GDN_IN(f + c * 128, 16, bq, st) ? gdndev::ld4(f + c * 128) : make_float4(0.f, 0.f, 0.f, 0.f);
+            o[r][c] = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
     }
     if (s1 > ctx) gdnattn::root_paths(a, b, s.path, s.parent, tid, kThreads, part == parts - 1, [] { __syncthreads(); });
-    float m[R], l[R], o[R][kCols];
+    // this lane's scores of a step: places own0 + i, slot place / R, row place % R
+    const int own0 = F::kScores >= F::kLanes ? sub * kOwn : sub / F::kSame;
+    float m[kOwn], l[kOwn];
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-        m[r] = -INFINITY, l[r] = 0.f;
+    for (int i = 0; i < kOwn; ++i) m[i] = -INFINITY, l[i] = 0.f;
+    float *pw = s.p[warp][grp];
+#pragma unroll 1
+    for (; base < s1; base += kBlock) {
+        float x[F::kScores];
 #pragma unroll
-        for (int c = 0; c < kCols; ++c) o[r][c] = 0.f;
-    }
-    for (int base = s0, buf = 0; base < s1; base += kTile, buf ^= 1) {
-        if (base + kTile < s1) {
-            fetch(base + kTile, buf ^ 1);
-            asm volatile("cp.async.wait_group 1;" ::: "memory");
-        } else {
-            asm volatile("cp.async.wait_group 0;" ::: "memory");
-        }
-        __syncthreads();
-        if (row0 + warp * R < rows) {
-            float sc[R] = {};
-#pragma unroll 4
-            for (int c = 0; c < D; c += 4) {
-                const float4 kk = *reinterpret_cast<const float4 *>(&s.k[buf][lane][c]);
-#pragma unroll
-                for (int r = 0; r < R; ++r)
-                    sc[r] = gdndev::dot4(*reinterpret_cast<const float4 *>(&s.q[warp * R + r][c]), kk, sc[r]);
-            }
-            const int slot = base + lane;
-            const bool edge = base + kTile > ctx;
+        for (int u = 0; u < kU; ++u)
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-                const int row = row0 + warp * R + r;
-                const bool seen = !edge || (slot < s1 && (slot < ctx || (row < rows && (s.path[row / group] >> (slot - ctx) & 1))));
-                const float x = seen ? sc[r] * a.scale_log2 : -INFINITY;
-                float top = x;
+                x[u * R + r] = 0.f;
 #pragma unroll
-                for (int w = 16; w; w >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, w));
-                const float m2 = fmaxf(m[r], top), mm = m2 == -INFINITY ? 0.f : m2;
-                const float scale = exp2f(m[r] - mm), p = exp2f(x - mm);
-                m[r] = m2;
-                l[r] = l[r] * scale + p;
-#pragma unroll
-                for (int c = 0; c < kCols; ++c) o[r][c] *= scale;
-                s.p[warp * R + r][lane] = seen ? p : -1.f;  // below zero: not in the sum, whatever v holds
+                for (int c = 0; c < kC; ++c) x[u * R + r] = gdndev::dot4(q[r][c], k[u][c], x[u * R + r]);
             }
+        place = place_of(base + kBlock, next);
+        next = page_of(base + 2 * kBlock);
+        load(k, kp, bk, place);
+        sum_apart<F::kScores, F::kLanes / 2>(x, lane);
+        const bool edge = base + F::kStep > ctx;
+        float scale[kOwn];
+        bool moved = false;
+#pragma unroll
+        for (int i = 0; i < kOwn; ++i) {
+            const int r = (own0 + i) % R, slot = base + (own0 + i) / R * kG + grp, row = row0 + r;
+            const bool seen = !edge || (slot < s1 && (slot < ctx || (row < rows && (s.path[row / group] >> (slot - ctx) & 1))));
+            const float score = seen ? x[i] * a.scale_log2 : -INFINITY;
+            float top = score;
+#pragma unroll
+            for (int w = F::kSame * R / kOwn; w < 32; w *= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, w));
+            const float m2 = fmaxf(m[i], top), mm = m2 == -INFINITY ? 0.f : m2, p = exp2f(score - mm);
+            scale[i] = exp2f(m[i] - mm);
+            moved |= m2 != m[i];
+            m[i] = m2;
+            l[i] = l[i] * scale[i] + p;
+            pw[own0 + i] = seen ? p : -1.f;  // below zero: not in the sum, whatever v holds
+        }
+        if (__any_sync(~0u, moved)) {
+#pragma unroll
+            for (int i = 0; i < kOwn; ++i) s.scale[warp][(own0 + i) % R] = scale[i];
             __syncwarp();
-#pragma unroll 1
-            for (int j = 0; j < kTile; j += 4) {
-                float4 p[R];
 #pragma unroll
-                for (int r = 0; r < R; ++r) p[r] = *reinterpret_cast<const float4 *>(&s.p[warp * R + r][j]);
+            for (int r = 0; r < R; ++r) {
+                const float f = s.scale[warp][r];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    float vv[kCols];
+                for (int c = 0; c < kC; ++c) o[r][c] = make_float4(o[r][c].x * f, o[r][c].y * f, o[r][c].z * f, o[r][c].w * f);
+            }
+        }
+        __syncwarp();
 #pragma unroll
-                    for (int c = 0; c < kCols; ++c) vv[c] = s.v[buf][j + i][lane + c * 32];
+        for (int u = 0; u < kU; ++u)
 #pragma unroll
-                    for (int r = 0; r < R; ++r) {
-                        const float w = i == 0 ? p[r].x : i == 1 ? p[r].y : i == 2 ? p[r].z : p[r].w;
-                        if (!edge || w >= 0.f || w != w)
+            for (int r = 0; r < R; ++r) {
+                const float w = pw[u * R + r];
+                if (!edge || w >= 0.f || w != w)
 #pragma unroll
-                            for (int c = 0; c < kCols; ++c) o[r][c] = fmaf(w, vv[c], o[r][c]);
+                    for (int c = 0; c < kC; ++c) {
+                        o[r][c].x = fmaf(w, v[u][c].x, o[r][c].x);
+                        o[r][c].y = fmaf(w, v[u][c].y, o[r][c].y);
+                        o[r][c].z = fmaf(w, v[u][c].z, o[r][c].z);
+                        o[r][c].w = fmaf(w, v[u][c].w, o[r][c].w);
                     }
-                }
             }
-        }
-        __syncthreads();  // the buffer is fetched into again
+        __syncwarp();  // the weights' and scales' places are written again
+        load(v, vp, bv, place);
+    }
+    // the warps' sums on one scale
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i) {
+        float sum = l[i];
+#pragma unroll
+        for (int w = F::kSame * R / kOwn; w < 32; w *= 2) sum += __shfl_xor_sync(~0u, sum, w);
+        s.m[warp][(own0 + i) % R] = m[i];
+        s.l[warp][(own0 + i) % R] = sum;
     }
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-        float sum = l[r];
+    for (int r = 0; r < R; ++r)
 #pragma unroll
-        for (int w = 16; w; w >>= 1) sum += __shfl_xor_sync(~0u, sum, w);
-        const int row = row0 + warp * R + r;
-        if (row < rows) {
-            const int t = row / group, h = kv * group + row % group;
-            const size_t at = (((size_t)b * a.n_tok + t) * a.h_q + h) * parts + part;
-            if (lane == 0 && GDN_IN(part_ms + at, 8, bms, st)) part_ms[at] = make_float2(m[r], sum);
-#pragma unroll
-            for (int c = 0; c < kCols; ++c) {
-                float *to = part_o + at * D + lane + c * 32;
-                if (GDN_IN(to, 4, bo, st)) *to = o[r][c];
+        for (int c = 0; c < kC; ++c) {
+            if (kG == 2) {
+                o[r][c].x += __shfl_xor_sync(~0u, o[r][c].x, 16);
+                o[r][c].y += __shfl_xor_sync(~0u, o[r][c].y, 16);
+                o[r][c].z += __shfl_xor_sync(~0u, o[r][c].z, 16);
+                o[r][c].w += __shfl_xor_sync(~0u, o[r][c].w, 16);
             }
+            if (grp == 0) *reinterpret_cast<float4 *>(&s.o[warp][r][c * 128 + sub * 4]) = o[r][c];
         }
+    __syncthreads();
+    for (int i = tid; i < R * (D / 4); i += kThreads) {
+        const int r = i / (D / 4), c = i % (D / 4) * 4, row = row0 + r;
+        if (row >= rows) break;
+        float top = -INFINITY, sum = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s.m[w][r]);
+        const float mm = top == -INFINITY ? 0.f : top;
+        float4 all = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            const float f = exp2f(s.m[w][r] - mm);  // 0 for a warp that had no slot
+            const float4 y = *reinterpret_cast<const float4 *>(&s.o[w][r][c]);
+            sum = fmaf(s.l[w][r], f, sum);
+            all = make_float4(fmaf(y.x, f, all.x), fmaf(y.y, f, all.y), fmaf(y.z, f, all.z), fmaf(y.w, f, all.w));
+        }
+        const int t = row / group, h = kv * group + row % group;
+        const size_t at = (((size_t)b * a.n_tok + t) * a.h_q + h) * parts + part;
+        if (c == 0 && GDN_IN(part_ms + at, 8, bms, st)) part_ms[at] = make_float2(top, sum);
+        float *to = part_o + at * D + c;
+        if (GDN_IN(to, 16, bo, st)) *reinterpret_cast<float4 *>(to) = all;
     }
+}
+
+__device__ __forceinline__ void copy16(void *to, const void *from, bool there) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((unsigned)__cvta_generic_to_shared(to)), "l"(from),
+                 "r"(there ? 16 : 0)
+                 : "memory");  // zeros where there is nothing to copy
 }
 
 // Many rows: a warp takes 4 R rows and its own tile of 32 slots, a lane R rows by
@@ -470,7 +539,7 @@ __global__ void __launch_bounds__(256) join_parts(AttnArgs a, int parts, const f
     }
 }
 
-int rows_per_warp(int rows) { return rows <= kWarps ? 1 : rows <= 2 * kWarps ? 2 : 4; }
+int few_rows(int rows) { return rows <= 1 ? 1 : rows <= 2 ? 2 : rows <= 4 ? 4 : 8; }
 
 // Whether attend_many() takes a call, and how: a lane's rows (R), the warps side
 // by side in rows, the parts that a request's slots are cut into by blocks, and
@@ -479,37 +548,35 @@ struct Cut {
     int lane_rows, row_warps, row_blocks, parts, pieces;
 };
 
-// attend_many() from one row more on than the other kernel's warps hold with two
-// each; heads of 256, whose tiles leave it no room for less than 64 rows, from 33 on.
+// attend() holds eight rows in registers and reads the cache again for the next
+// eight: attend_many() from nine rows on (8 requests of 16 rows, 4 heads of 128 over
+// 3,000 slots: 55 us against 57); heads of 256, whose tiles leave it no room for less
+// than 64 rows, from 33 on (2 requests of 28 rows over 3,000: 55 against 29).
 Cut cut_of(const attn_dims *dims, int n_tok) {
-    const int batch = dims->batch, h_kv = dims->h_kv, d = dims->d_head;
-    const int rows = n_tok * (dims->h_q / h_kv), few = d == 256 ? 4 * kWarps : 2 * kWarps;
-    const int64_t slots = (int64_t)dims->table_width * dims->page_tokens;
+    const int d = dims->d_head, rows = n_tok * (dims->h_q / dims->h_kv);
+    const int64_t slots = (int64_t)dims->table_width * dims->page_tokens;  // the longest request that the table holds
     Cut c{};
-    if (rows <= few) {
-        // enough blocks for the GPU, and no part under four tiles of the longest request that the table holds
-        const int block = kWarps * rows_per_warp(rows);
-        const int64_t blocks = (int64_t)((rows + block - 1) / block) * batch * h_kv;
-        const int64_t most = (slots + 4 * kTile - 1) / (4 * kTile), parts = (4 * 152 + blocks - 1) / blocks;
+    int tile, held = 152, slot_warps = 1;  // slots that a block takes at a time, blocks that the GPU holds
+    if (rows <= (d == 256 ? 32 : 8)) {
+        const int block = few_rows(rows);
         c.row_blocks = (rows + block - 1) / block;
-        c.parts = (int)(parts > most ? most : parts);
-        c.parts = c.parts > kMaxParts ? kMaxParts : c.parts < 1 ? 1 : c.parts;
-        c.pieces = c.parts;
-        return c;
+        tile = 128;
+        if (block < 8 && d < 256) held = 304;
+    } else {
+        c.lane_rows = d == 256 || rows <= 32 ? 4 : 8;
+        // the fewest rows of padding, then the fewest copies of a tile
+        for (int w = kWarps; w >= (d == 256 ? 4 : 2); w /= 2) {
+            const int block = w * 4 * c.lane_rows, blocks = (rows + block - 1) / block;
+            if (!c.row_warps || blocks * w < c.row_blocks * c.row_warps) c.row_warps = w, c.row_blocks = blocks;
+        }
+        slot_warps = kWarps / c.row_warps;
+        tile = kTile * slot_warps;
     }
-    c.lane_rows = d == 256 || rows <= 32 ? 4 : 8;
-    // the fewest rows of padding, then the fewest copies of a tile
-    for (int w = kWarps; w >= (d == 256 ? 4 : 2); w /= 2) {
-        const int block = w * 4 * c.lane_rows, blocks = (rows + block - 1) / block;
-        if (!c.row_warps || blocks * w < c.row_blocks * c.row_warps) c.row_warps = w, c.row_blocks = blocks;
-    }
-    // one block of an SM at a time: the parts whose rounds of blocks take the fewest tiles, half a
-    // tile counted for a block's start and end
-    const int slot_warps = kWarps / c.row_warps;
-    const int64_t tiles = (slots + kTile * slot_warps - 1) / (kTile * slot_warps), units = (int64_t)c.row_blocks * batch * h_kv;
+    // the parts whose rounds of blocks take the fewest tiles, half a tile counted for a block's start and end
+    const int64_t tiles = (slots + tile - 1) / tile, units = (int64_t)c.row_blocks * dims->batch * dims->h_kv;
     int64_t best = INT64_MAX;
-    for (int p = 1; p <= kMaxParts / slot_warps && (p == 1 || 2 * p <= tiles); ++p) {
-        const int64_t cost = (units * p + 151) / 152 * (2 * ((tiles + p - 1) / p) + 1);
+    for (int p = 1; p <= kMaxParts / slot_warps && (p == 1 || p <= tiles); ++p) {
+        const int64_t cost = (units * p + held - 1) / held * (2 * ((tiles + p - 1) / p) + 1);
         if (cost < best) best = cost, c.parts = p;
     }
     c.pieces = c.parts * slot_warps;
@@ -527,7 +594,7 @@ bool allow_smem(Kernel kernel, size_t bytes, bool (&set)[256]) {
 
 template <int D, int R>
 bool launch_few(const AttnArgs &a, const Cut &c, float *o, float2 *ms, cudaStream_t st) {
-    constexpr size_t kSmem = sizeof(Shared<D, R>);
+    constexpr size_t kSmem = sizeof(typename Few<D, R>::Smem);
     static bool set[256] = {};
     return allow_smem(attend<D, R>, kSmem, set) &&
            gdndev::launch_pdl(attend<D, R>, dim3(c.row_blocks, a.batch * a.h_kv, c.parts), dim3(kThreads), kSmem, st, a, c.parts, o,
@@ -553,13 +620,16 @@ int launch(const AttnArgs &a, const Cut &c, void *ws, cudaStream_t st) {
     float2 *ms = static_cast<float2 *>(ws);
     float *o = reinterpret_cast<float *>(static_cast<char *>(ws) + ((size_t)out_rows * c.pieces * 8 + 255) / 256 * 256);
     bool ok;
-    if constexpr (D == 256) {
-        const int r = rows_per_warp(a.n_tok * (a.h_q / a.h_kv));
-        ok = c.lane_rows ? launch_many<D, 4>(a, c, o, ms, st) : r == 1 ? launch_few<D, 1>(a, c, o, ms, st)
-           : r == 2 ? launch_few<D, 2>(a, c, o, ms, st) : launch_few<D, 4>(a, c, o, ms, st);
+    if (c.lane_rows) {
+        if constexpr (D == 256) ok = launch_many<D, 4>(a, c, o, ms, st);
+        else ok = c.lane_rows == 8 ? launch_many<D, 8>(a, c, o, ms, st) : launch_many<D, 4>(a, c, o, ms, st);
     } else {
-        ok = c.lane_rows == 8 ? launch_many<D, 8>(a, c, o, ms, st) : c.lane_rows == 4 ? launch_many<D, 4>(a, c, o, ms, st)
-           : rows_per_warp(a.n_tok * (a.h_q / a.h_kv)) == 1 ? launch_few<D, 1>(a, c, o, ms, st) : launch_few<D, 2>(a, c, o, ms, st);
+        switch (few_rows(a.n_tok * (a.h_q / a.h_kv))) {
+            case 1: ok = launch_few<D, 1>(a, c, o, ms, st); break;
+            case 2: ok = launch_few<D, 2>(a, c, o, ms, st); break;
+            case 4: ok = launch_few<D, 4>(a, c, o, ms, st); break;
+            default: ok = launch_few<D, 8>(a, c, o, ms, st);
+        }
     }
     if (!ok) return GDN_ERR_CUDA;
     return gdndev::launch_pdl(join_parts<D>, dim3((unsigned)((out_rows + 7) / 8)), dim3(256), 0, st, a, c.pieces, (const float *)o,

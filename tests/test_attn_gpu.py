@@ -247,6 +247,23 @@ def test_attention_many_rows_over_long_contexts(dtype, d, T, h_q, h_kv, n):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("T,h_q,h_kv", [(1, 2, 2), (2, 3, 3), (1, 6, 2), (4, 1, 1), (3, 4, 2), (2, 8, 2), (10, 2, 2)])
+def test_attention_few_rows_over_long_contexts(dtype, d, T, h_q, h_kv):
+    g = np.random.default_rng(T * d + h_q)
+    ctx = [2741, 0, 127, 1030]
+    cache, q, parents = make(g, ctx, T, h_q, h_kv, d, 32, dtype, T > 1)
+    n = ctx[0] + T
+    k, v = cache.rows(0, np.arange(n))
+    cache.put(0, np.arange(n), k.float() * torch.linspace(0.2, 4.0, n, device="cuda")[:, None, None], v)
+    out, st = attend(cache, q, parents, d ** -0.5)
+    check(cache, q, parents, out, d ** -0.5)
+    assert int(st.item()) == 0
+    again, _ = attend(cache, q, parents, d ** -0.5)
+    assert torch.equal(out, again)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("d", [64, 256])
 def test_attention_many_rows_leave_out_lengths_and_flag_pages(dtype, d):
     g = np.random.default_rng(15)
