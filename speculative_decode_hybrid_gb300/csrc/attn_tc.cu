@@ -20,9 +20,9 @@
 // gathered page by page), one that issues each of the products. S is double:
 // the scores of the next tile are computed while the softmax works on this one.
 //
-// More than 128 rows: clusters of P = 2 blocks, an M tile each, over the same
-// tiles; each block loads half of a tile's boxes into both (TMA multicast), so
-// that what leaves L2 is read once.
+// More than 128 rows: P = 2 neighbouring blocks take an M tile each of the same
+// piece of work. They load the same tiles at about the same time, each for
+// itself: the second one's come from L2.
 //
 // Work is split over the whole flattened list of (request, head, M tiles, slot
 // tile): block i of n takes the i-th n-th of it, whatever the requests'
@@ -36,10 +36,10 @@
 // copy rate, of which 6 us pass before the first tile has come; 22 nodes x 8 heads,
 // 256 wide, over 32,501 slots (67 MB) 26 us: thirteen tiles a block, each some
 // 1,850 cycles apart (1.6 us from asking for a tile to having it, three in
-// flight), after 6 us until the first. Two M tiles in one block instead of a
-// cluster: 55 us instead of 42.5 for 512 rows over up to 8,000 slots, as tensor
-// memory then leaves room for single S buffers only, and a tile's products and
-// softmax follow one another.
+// flight), after 6 us until the first. Two M tiles in one block
+// instead of two blocks: 55 us instead of 43 for 512 rows over up to 8,000 slots,
+// as tensor memory then leaves room for single S buffers only, and a tile's
+// products and softmax follow one another.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -79,7 +79,7 @@ struct Shape {
 struct Plan {
     int group, rows;        // query heads of a key/value head; rows of one key/value head
     int m_groups, units;    // groups of P M tiles of a head; units (head, group) of a request
-    int blocks;             // clusters of P blocks
+    int blocks;             // groups of P blocks, each group on a share of its own
     unsigned by_group, by_m_groups, by_blocks;  // 2^32 / n rounded up: x / n for x * n < 2^32
 };
 
@@ -198,18 +198,6 @@ __device__ __forceinline__ void load_box(unsigned dst, const CUtensorMap *map, i
         "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
         : "memory");
 }
-// Into both blocks of a cluster of two, at this place, and counted by the barrier there.
-__device__ __forceinline__ void load_box_pair(unsigned dst, const CUtensorMap *map, int x, int y, int z, unsigned bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster [%0], [%1, {%2, %3, "
-        "%4}], [%5], %6;" ::"r"(dst),
-        "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar), "h"((unsigned short)3)
-        : "memory");
-}
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
-}
-
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -268,7 +256,7 @@ attend(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtens
     __shared__ Control<D> c;
     char *base = raw + ((1024 - (saddr(raw) & 1023)) & 1023);
     const unsigned k_s = saddr(base), v_s = k_s + kStages * S::kTileBytes, pass_s = v_s + kStages * S::kTileBytes;
-    const int cluster = blockIdx.x / P, rank = blockIdx.x % P;
+    const int share = blockIdx.x / P, rank = blockIdx.x % P;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int group = plan.group, rows = plan.rows;
     int32_t *st = a.status;
@@ -280,9 +268,9 @@ attend(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtens
     if (tid == 0) {
         for (int i = 0; i < kStages; ++i) {
             bar_init(saddr(&c.k_full[i]), 1);
-            bar_init(saddr(&c.k_empty[i]), P);  // a stage is free once both blocks have used it
+            bar_init(saddr(&c.k_empty[i]), 1);
             bar_init(saddr(&c.v_full[i]), 1);
-            bar_init(saddr(&c.v_empty[i]), P);
+            bar_init(saddr(&c.v_empty[i]), 1);
         }
         for (int i = 0; i < 2; ++i) {
             bar_init(saddr(&c.s_full[i]), 1);
@@ -292,25 +280,24 @@ attend(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtens
         bar_init(saddr(&c.q_full), 4);
         bar_init(saddr(&c.drain[0]), 1);
         bar_init(saddr(&c.drain[1]), 1);
-        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");  // for the TMA unit
         c.quit = 0;
         for (int i = 0; i < 4; ++i) c.odd_nodes[i] = 0;
     }
     gdntc::fence_before_sync();
     __syncthreads();
-    if (P == 2) cluster_sync();  // the other block's barriers are there
     gdntc::fence_after_sync();
     const unsigned tmem = c.tmem;
     gdndev::pdl_launch_dependents();
     gdndev::pdl_wait();
-    Work work = block_work<kN>(a, plan, cluster, blockIdx.x == 0 && warp == 0);
-    if (tid == 0 && rank == 0) pieces.unit[2 * cluster] = pieces.unit[2 * cluster + 1] = -1;
+    Work work = block_work<kN>(a, plan, share, blockIdx.x == 0 && warp == 0);
+    if (tid == 0 && rank == 0) pieces.unit[2 * share] = pieces.unit[2 * share + 1] = -1;
     volatile int *quit = &c.quit;
     constexpr unsigned kSCol = S::kSCol, kQCol = S::kQCol;
 
     if (warp == kTmaWarp) {
         int g = 0;  // tiles so far
-        const int page_rows = min(1 << a.page_shift, kN / P), boxes = kN / page_rows;
+        const int page_rows = min(1 << a.page_shift, kN), boxes = kN / page_rows;
         const unsigned box_bytes = page_rows * 128u;
         const int mine = lane / S::kChunks, chunk = lane % S::kChunks;  // this lane's page of the tile, and its column chunk
         const Buf bt{a.table, (size_t)a.batch * a.width * 4};
@@ -346,9 +333,7 @@ attend(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtens
                     if (!ok) break;
                     if (lane == 0) bar_expect(full, bytes);
                     __syncwarp();
-                    if (P == 1 && used) load_box((half ? v_s : k_s) + at, half ? &v_map : &k_map, chunk * 64, y, z, full);
-                    if (P == 2 && used && (mine & 1) == rank)  // the other boxes come from the other block
-                        load_box_pair((half ? v_s : k_s) + at, half ? &v_map : &k_map, chunk * 64, y, z, full);
+                    if (used) load_box((half ? v_s : k_s) + at, half ? &v_map : &k_map, chunk * 64, y, z, full);
                 }
                 if (!ok) break;
                 page = next;
@@ -391,8 +376,7 @@ attend(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtens
                         gdntc::mma_bf16_ts(tmem + kSCol + slot * kN, tmem + kQCol + i * 8,
                                            gdntc::smem_desc_sw128(k + (i / 4) * (kN * 128) + (i % 4) * 32), kIdS, i > 0);
                     gdntc::mma_commit(saddr(&c.s_full[slot]));
-                    if (P == 2) gdntc::mma_commit_pair(saddr(&c.k_empty[stage]));
-                    else gdntc::mma_commit(saddr(&c.k_empty[stage]));
+                    gdntc::mma_commit(saddr(&c.k_empty[stage]));
                 }
             }
             gdntc::mma_commit(saddr(&c.drain[0]));
@@ -420,8 +404,7 @@ attend(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtens
                         gdntc::mma_bf16_ts(tmem, tmem + kSCol + slot * kN + i * 8, gdntc::smem_desc_sw128_mn(v + i * 2048, kN * 128),
                                            kIdO, j > 0 || i > 0);
                     gdntc::mma_commit(saddr(&c.pv_done[slot]));
-                    if (P == 2) gdntc::mma_commit_pair(saddr(&c.v_empty[stage]));
-                    else gdntc::mma_commit(saddr(&c.v_empty[stage]));
+                    gdntc::mma_commit(saddr(&c.v_empty[stage]));
                 }
             }
             gdntc::mma_commit(saddr(&c.drain[1]));
@@ -637,7 +620,7 @@ attend(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtens
                 const bool whole = s.n == s.tiles;
                 const float total = sum.x + sum.y, inv = whole ? 1.f / total : 1.f;
                 const unsigned long long odd = *(volatile unsigned long long *)&c.odd_nodes[seg & 3] & path;
-                const size_t piece = 2 * cluster + (first_segment ? 0 : 1);
+                const size_t piece = 2 * share + (first_segment ? 0 : 1);
                 const int pr = rank * kM + tid;
                 const Buf bo{pieces.o, (size_t)2 * plan.blocks * P * kM * D * 4}, bms{pieces.ms, (size_t)2 * plan.blocks * P * kM * 8};
                 if (!whole && tid == 0 && rank == 0) pieces.unit[piece] = s.b * plan.units + s.unit;
@@ -705,7 +688,6 @@ attend(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtens
                 if (GDN_IN(to + i, 16, bout, st)) to[i] = make_uint4(0, 0, 0, 0);
         }
     __syncthreads();
-    if (P == 2) cluster_sync();  // the other block may still load into this one's shared memory
     if (c.quit && tid == 0 && st) atomicOr(st, GDN_DEV_SCHED);
     if (warp == kScoreWarp) {
         gdntc::fence_after_sync();
@@ -866,7 +848,7 @@ int block_count() {
     return sms <= 0 ? 152 : sms < kMaxBlocks ? sms : kMaxBlocks;
 }
 
-// Blocks of a cluster: two where there is more than one M tile.
+// Blocks side by side on the same tiles: two where there is more than one M tile.
 int pair(const attn_dims *d, int n_tok) { return n_tok * (d->h_q / d->h_kv) > kM ? 2 : 1; }
 
 template <int D, int P>
@@ -881,7 +863,7 @@ int launch(const attn_dims *d, const AttnArgs &a, void *ws, cudaStream_t st) {
         set[dev] = true;
     }
     CUtensorMap k_map, v_map;
-    if (!pool_map(&k_map, d, a.k_pages, S::kN / P) || !pool_map(&v_map, d, a.v_pages, S::kN / P)) return GDN_ERR_CUDA;
+    if (!pool_map(&k_map, d, a.k_pages, S::kN) || !pool_map(&v_map, d, a.v_pages, S::kN)) return GDN_ERR_CUDA;
     const int blocks = block_count() / P;
     char *at = static_cast<char *>(ws);
     const size_t rows_of_pieces = (size_t)2 * blocks * P * kM;
@@ -890,8 +872,7 @@ int launch(const attn_dims *d, const AttnArgs &a, void *ws, cudaStream_t st) {
     const int group = a.h_q / a.h_kv, rows = a.n_tok * group, m_groups = (rows + P * kM - 1) / (P * kM);
     auto by = [](int n) { return (unsigned)(((1ull << 32) + n - 1) / n); };
     const Plan plan{group, rows, m_groups, a.h_kv * m_groups, blocks, by(group), by(m_groups), by(blocks)};
-    if (gdndev::launch_pdl_clusters(attend<D, P>, P, dim3(blocks * P), dim3(S::kThreads), S::kSmem, st, k_map, v_map, a, plan, pieces) !=
-        cudaSuccess)
+    if (gdndev::launch_pdl(attend<D, P>, dim3(blocks * P), dim3(S::kThreads), S::kSmem, st, k_map, v_map, a, plan, pieces) != cudaSuccess)
         return GDN_ERR_CUDA;
     // a unit has about blocks / units pieces, and one more
     const int64_t units = (int64_t)a.batch * plan.units;

@@ -45,36 +45,22 @@ __device__ __forceinline__ bool in_buf(const void *ptr, size_t n, Buf b, int32_t
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
-template <typename... KArgs, typename... Args>
-cudaError_t launch_pdl_clusters(void (*kern)(KArgs...), unsigned cluster, dim3 grid, dim3 block, size_t smem, cudaStream_t st,
-                                Args &&...args);
-
 // Launch `kern` with programmatic stream serialization, so that its launch
 // and scheduling overlap the tail of the previous kernel on the stream
 // (which pdl_wait() in `kern` then waits for).
 template <typename... KArgs, typename... Args>
 cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
                        Args &&...args) {
-    return launch_pdl_clusters(kern, 1, grid, block, smem, st, static_cast<Args &&>(args)...);
-}
-
-// ... in thread-block clusters of `cluster` blocks along x.
-template <typename... KArgs, typename... Args>
-cudaError_t launch_pdl_clusters(void (*kern)(KArgs...), unsigned cluster, dim3 grid, dim3 block, size_t smem, cudaStream_t st,
-                                Args &&...args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = block;
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
-    cudaLaunchAttribute attr[2];
+    cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = cluster;
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kern, static_cast<Args &&>(args)...);
 }
 

@@ -131,14 +131,6 @@ __device__ __forceinline__ void mma_commit(unsigned bar) {
                  : "memory");
 }
 
-// The same for the mbarrier at this place in both blocks of a cluster of two.
-__device__ __forceinline__ void mma_commit_pair(unsigned bar) {
-    asm volatile(
-        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-        "h"((unsigned short)3)
-        : "memory");
-}
-
 // Wait (bounded) for phase `parity` of the mbarrier at `bar`; false if the
 // wait gave up.
 __device__ __forceinline__ bool mbar_wait(unsigned bar, unsigned parity, unsigned polls) {
