@@ -262,7 +262,6 @@ attend(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtens
     int32_t *st = a.status;
     constexpr int kTmaWarp = 4, kScoreWarp = 5, kSumWarp = 6;
 
-    if (warp == kScoreWarp) gdntc::tmem_alloc<kTmemCols>(&c.tmem);
     if (warp == kTmaWarp && lane < 2)
         asm volatile("prefetch.tensormap [%0];" ::"l"(lane ? &v_map : &k_map) : "memory");
     if (tid == 0) {
@@ -284,13 +283,16 @@ attend(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtens
         c.quit = 0;
         for (int i = 0; i < 4; ++i) c.odd_nodes[i] = 0;
     }
+    gdndev::pdl_launch_dependents();  // join_pieces, which takes no tensor memory
+    gdndev::pdl_wait();
+    // All of the SM's columns, and only once nothing is waited for outside of this
+    // block: the kernel before may be anybody's, and may need columns itself.
+    if (warp == kScoreWarp) gdntc::tmem_alloc<kTmemCols>(&c.tmem);
     gdntc::fence_before_sync();
+    Work work = block_work<kN>(a, plan, share, blockIdx.x == 0 && warp == 0);
     __syncthreads();
     gdntc::fence_after_sync();
     const unsigned tmem = c.tmem;
-    gdndev::pdl_launch_dependents();
-    gdndev::pdl_wait();
-    Work work = block_work<kN>(a, plan, share, blockIdx.x == 0 && warp == 0);
     if (tid == 0 && rank == 0) pieces.unit[2 * share] = pieces.unit[2 * share + 1] = -1;
     volatile int *quit = &c.quit;
     constexpr unsigned kSCol = S::kSCol, kQCol = S::kQCol;

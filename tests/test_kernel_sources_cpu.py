@@ -24,3 +24,10 @@ def test_no_load_is_multicast():
     for path in SOURCES:
         for copy in re.findall(r'"[^"]*cp\.async\.bulk[^"]*"', code(path)):
             assert "multicast" not in copy, (os.path.basename(path), copy)
+
+
+def test_attention_takes_tensor_memory_after_the_grid_wait():
+    """A block that holds all of an SM's columns while it waits for the kernel
+    before would hang with one that allocates after letting it start."""
+    text = code(os.path.join(B.CSRC, "attn_tc.cu"))
+    assert text.count("tmem_alloc") == 1 and 0 < text.index("pdl_wait()") < text.index("tmem_alloc")
