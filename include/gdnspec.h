@@ -575,7 +575,7 @@ size_t attn_workspace_bytes(const attn_dims *dims, int32_t n_tok);
  *   accepted node.
  *   workspace  at least spec_accept_sample_workspace_bytes(B, N) bytes,
  *              256-byte aligned, any contents; overlapping calls must not share it
- * Limits: 1 <= N <= GDN_MAX_TOKENS + 1, 1 <= V < 2^31, B <= 65535.
+ * Limits: 1 <= N <= GDN_MAX_TOKENS + 1, 1 <= V <= 2^30, B <= 65535.
  * Returns GDN_OK or GDN_ERR_{NULL,DIMS,ALIGN,WORKSPACE,CUDA}.
  */
 int spec_accept_sample(int32_t batch, int32_t n_nodes, int32_t vocab, const float *logits,

@@ -54,6 +54,9 @@ constexpr int kMaxPieces = 40;      // blocks that a row may be spread over
 static_assert(kMaxPieces <= 64, "two pieces a lane");
 constexpr int kMinPart = 1024;      // values a block takes at least
 constexpr int kMaxNodes = GDN_MAX_TOKENS + 1;
+// Indexes of a row, and what is added to them (a slice's rounding, a pass of the
+// scan), are 32-bit.
+constexpr int kMaxVocab = 1 << 30;
 constexpr float kLog2e = 1.4426950408889634f;
 
 // A row's maximum and the sum of exp((x - max) / T).
@@ -502,7 +505,8 @@ extern "C" int spec_accept_sample(int32_t batch, int32_t n_nodes, int32_t vocab,
                                   int32_t *accept_len, int32_t *accept_node, int32_t *next_token,
                                   float *token_prob, void *workspace, size_t workspace_bytes,
                                   int32_t *dev_status, gdn_stream_t stream) {
-    if (batch < 1 || batch > 65535 || n_nodes < 1 || n_nodes > kMaxNodes || vocab < 1) return GDN_ERR_DIMS;
+    if (batch < 1 || batch > 65535 || n_nodes < 1 || n_nodes > kMaxNodes || vocab < 1 || vocab > kMaxVocab)
+        return GDN_ERR_DIMS;
     if (!logits || !tokens || !uniforms || !noise || !accept_len || !accept_node || !next_token) return GDN_ERR_NULL;
     using gdnhost::aligned_to;
     for (const void *p : {(const void *)logits, (const void *)draft_probs, (const void *)tokens, (const void *)parent_dev,
