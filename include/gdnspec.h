@@ -526,7 +526,9 @@ int attn_qk_norm_rope(const attn_dims *dims, int32_t n_tok, const void *qkv, int
  * bf16: products on the tensor cores with f32 accumulation, softmax in f32, its
  * weights rounded to bf16 for the second product; f32: all in f32.
  * Limits: 1 <= n_tok <= GDN_MAX_TOKENS, batch * h_kv <= 65535,
- * scale finite and above 0.
+ * scale finite and above 0; bf16: ceil(table_width * page_tokens / 64) * h_kv *
+ * ceil(n_tok * (h_q / h_kv) / 128), a request's most tiles of 64 slots and 128
+ * rows, below 2^31, and times batch below 2^34.
  * Returns GDN_OK or GDN_ERR_{NULL,DIMS,ALIGN,DTYPE,TREE_*,WORKSPACE,CUDA}.
  */
 int attn_verify_span(const attn_dims *dims, int32_t n_tok, const void *q, const void *k_pages,

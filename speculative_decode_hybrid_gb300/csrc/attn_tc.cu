@@ -890,6 +890,14 @@ int launch(const attn_dims *d, const AttnArgs &a, void *ws, cudaStream_t st) {
 
 namespace gdnattn {
 
+bool tc_fits(const attn_dims *d, int n_tok) {
+    // tiles of 64 slots (128-slot tiles and pairs of M tiles are fewer): Work::off
+    // counts a request's in an int, Work::left a block's share of all (16 blocks at least)
+    const int64_t rows = (int64_t)n_tok * (d->h_q / d->h_kv), slot_tiles = ((int64_t)d->table_width * d->page_tokens + 63) / 64;
+    const int64_t tiles = slot_tiles * d->h_kv * ((rows + kM - 1) / kM);
+    return tiles < (1LL << 31) && tiles * d->batch < (1LL << 34);
+}
+
 size_t tc_workspace(const attn_dims *d, int n_tok) {
     const size_t p = pair(d, n_tok), blocks = block_count() / p;
     return 2 * blocks * (p * kM * (d->d_head * 4 + 8) + 4);

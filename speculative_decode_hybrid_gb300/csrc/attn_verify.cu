@@ -34,6 +34,7 @@ int attend(const attn_dims *dims, int32_t n_tok, const int32_t *parent_dev, cons
 int check(const attn_dims *dims, int32_t n_tok) {
     if (const int rc = gdnhost::check_attn(dims)) return rc;
     if (n_tok < 1 || n_tok > GDN_MAX_TOKENS || (int64_t)dims->batch * dims->h_kv > 65535) return GDN_ERR_DIMS;
+    if (dims->in_dtype == GDN_BF16 && !gdnattn::tc_fits(dims, n_tok)) return GDN_ERR_DIMS;
     return GDN_OK;
 }
 

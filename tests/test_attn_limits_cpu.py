@@ -33,3 +33,27 @@ def test_sample_vocabulary_limit(lib, batch, n):
     assert sample(lib, 2 ** 30, batch=batch, n=n) == G.GDN_ERR_WORKSPACE
     for v in (2 ** 30 + 1, 2 ** 31 - 2 ** 14, 2 ** 31 - 39, 2 ** 31 - 8, 2 ** 31 - 1):
         assert sample(lib, v, batch=batch, n=n) == G.GDN_ERR_DIMS, v
+
+
+def dims(**kw):
+    d = dict(batch=1, layers=1, h_q=8, h_kv=8, d_head=64, page_tokens=256, n_pages=40, table_width=9, dtype=G.GDN_BF16)
+    d.update(kw)
+    return G.make_attn_dims(*d.values())
+
+
+def span(lib, d, n_tok=1):
+    return lib.attn_verify_span(ctypes.byref(d), n_tok, *[FAKE] * 5, 0.1, FAKE, None, 0, None, None)
+
+
+@pytest.mark.parametrize("n_tok,fits,over", [
+    # a request's tiles of 64 slots x heads x 128-row groups reach 2^31 (a table may repeat a page)
+    (1, dict(h_q=1024, h_kv=512, table_width=2 ** 20 - 1), dict(h_q=1024, h_kv=512, table_width=2 ** 20)),
+    (64, dict(h_q=1024, h_kv=1, table_width=2 ** 20 - 1), dict(h_q=1024, h_kv=1, table_width=2 ** 20)),
+    # the requests' together reach 2^34
+    (1, dict(batch=31, h_q=1024, h_kv=1024, table_width=2 ** 17), dict(batch=32, h_q=1024, h_kv=1024, table_width=2 ** 17)),
+    (8, dict(batch=65535, h_q=64, h_kv=1, table_width=2 ** 14), dict(batch=65535, h_q=256, h_kv=1, table_width=2 ** 14))])
+def test_bf16_attention_tile_limit(lib, n_tok, fits, over):
+    assert span(lib, dims(**fits), n_tok) == G.GDN_ERR_WORKSPACE and G.attn_workspace_bytes(dims(**fits), n_tok) > 0
+    assert span(lib, dims(**over), n_tok) == G.GDN_ERR_DIMS and G.attn_workspace_bytes(dims(**over), n_tok) == 0
+    f32 = dims(**dict(over, dtype=G.GDN_F32))       # counts in 64 bits where it has to
+    assert span(lib, f32, n_tok) == G.GDN_ERR_WORKSPACE
