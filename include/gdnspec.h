@@ -80,6 +80,7 @@ typedef void *gdn_stream_t;
 #define GDN_ERR_WORKSPACE 10      /* workspace NULL, misaligned or smaller than required */
 #define GDN_ERR_CUDA 11           /* a CUDA launch or query failed */
 #define GDN_ERR_FLAGS 12          /* a flags argument has a bit this library does not define */
+#define GDN_ERR_OVERLAP 13        /* an output overlaps an input that it must not */
 
 /* Device-side status bits, OR-ed into *dev_status (int32, device memory). */
 #define GDN_DEV_TOKEN_RANGE 0x1   /* a draft token id outside [0, vocab): counted as a mismatch */
@@ -601,7 +602,7 @@ size_t spec_accept_sample_workspace_bytes(int32_t batch, int32_t n_nodes);
  *   k_pages, v_pages [Y][n_pages][h_kv][page_tokens][d_head]
  *   ctx_out      [B]; must not overlap ctx_len
  * Limits: 2 <= n_nodes <= GDN_MAX_TOKENS + 1.
- * Returns GDN_OK or GDN_ERR_{NULL,DIMS,ALIGN,DTYPE,CUDA}.
+ * Returns GDN_OK or GDN_ERR_{NULL,DIMS,ALIGN,DTYPE,OVERLAP,CUDA}.
  */
 int kv_commit_path(const attn_dims *dims, int32_t n_nodes, const int32_t *parent_dev,
                    const int32_t *accept_node, const int32_t *ctx_len, const int32_t *page_table,

@@ -96,6 +96,7 @@ extern "C" const char *gdn_status_str(int status) {
         case GDN_ERR_WORKSPACE: return "workspace missing, misaligned or too small";
         case GDN_ERR_CUDA: return "CUDA launch failed";
         case GDN_ERR_FLAGS: return "a flags argument has an undefined bit";
+        case GDN_ERR_OVERLAP: return "an output overlaps an input that it must not";
         default: return "unknown status";
     }
 }

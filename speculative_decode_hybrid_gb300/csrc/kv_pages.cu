@@ -14,6 +14,7 @@
 // pool and integer atomics, in whatever order, give the same result.
 #include <cuda_runtime.h>
 
+#include <cstdint>
 #include <initializer_list>
 
 #include "gdn_device.cuh"
@@ -455,6 +456,9 @@ extern "C" int kv_commit_path(const attn_dims *dims, int32_t n_nodes, const int3
     for (const void *p : {(const void *)parent_dev, (const void *)accept_node, (const void *)ctx_len,
                           (const void *)page_table, (const void *)ctx_out, (const void *)dev_status})
         if (!aligned_to(p, 4)) return GDN_ERR_ALIGN;
+    // a request's blocks read its length while the first of them writes the new one
+    const uintptr_t in = reinterpret_cast<uintptr_t>(ctx_len), out = reinterpret_cast<uintptr_t>(ctx_out);
+    if ((in > out ? in - out : out - in) < (uintptr_t)dims->batch * 4) return GDN_ERR_OVERLAP;
     CommitArgs a{n_nodes, log2_of(dims->page_tokens), dims->n_pages, dims->table_width,
                  log2_of((int)(dims->d_head * gdnhost::attn_elem_bytes(dims) / 16)), slices_of(dims, k_pages, v_pages),
                  parent_dev, accept_node, ctx_len, page_table, ctx_out, dev_status};

@@ -34,6 +34,7 @@ GDN_ERR_TREE_NOT_CHAIN = 9
 GDN_ERR_WORKSPACE = 10
 GDN_ERR_CUDA = 11
 GDN_ERR_FLAGS = 12
+GDN_ERR_OVERLAP = 13
 
 GDN_VERIFY_STATE_READY = 0x1
 GDN_ROPE_PAIRS = 0x1

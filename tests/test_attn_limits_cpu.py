@@ -57,3 +57,12 @@ def test_bf16_attention_tile_limit(lib, n_tok, fits, over):
     assert span(lib, dims(**over), n_tok) == G.GDN_ERR_DIMS and G.attn_workspace_bytes(dims(**over), n_tok) == 0
     f32 = dims(**dict(over, dtype=G.GDN_F32))       # counts in 64 bits where it has to
     assert span(lib, f32, n_tok) == G.GDN_ERR_WORKSPACE
+
+
+@pytest.mark.parametrize("parent", [None, FAKE])
+def test_commit_refuses_lengths_in_place(lib, parent):
+    """Blocks of a request would read the length that another has replaced."""
+    d = dims(batch=6)
+    for out in (FAKE, FAKE + 4, FAKE + 20, FAKE - 4, FAKE - 20):
+        assert lib.kv_commit_path(ctypes.byref(d), 4, parent, FAKE, FAKE, FAKE, FAKE, FAKE, out, None, None) == G.GDN_ERR_OVERLAP
+    assert "overlap" in G.status_str(G.GDN_ERR_OVERLAP)
