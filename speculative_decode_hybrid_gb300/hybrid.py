@@ -43,6 +43,12 @@ class AttnShape:
     max_tokens: int = 4096      # slots a request's page table holds
 
 
+def on_stream(stream):
+    """Context in which torch queues where the library's calls do: on the current
+    stream (None), a torch stream, or the stream of a handle."""
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
+
+
 class HybridStep:
     def __init__(self, wl: Workload, attn: AttnShape, ctx_len, temperature: float = 1.0, seed: int = 0, device="cuda"):
         """ctx_len: committed tokens of each request (their cache rows are
@@ -65,7 +71,7 @@ class HybridStep:
         self.table = torch.full((B, width), -1, dtype=torch.int32, device=dev)
         self.page_ref = torch.zeros((n_pages,), dtype=torch.int32, device=dev)
         self.ctx = torch.as_tensor(list(ctx_len), dtype=torch.int32).to(dev)
-        self.ctx_next = torch.empty_like(self.ctx)
+        self.ctx_next, self.want = torch.empty_like(self.ctx), torch.empty_like(self.ctx)
         # per layer and token the projected row [q | k | v], the norm weights
         self.row = (a.h_q + 2 * a.h_kv) * a.d_head
         self.qkv = normal(a.layers, B, T, self.row, dtype=dt)
@@ -102,8 +108,9 @@ class HybridStep:
 
     def make_room(self, stream=None):
         """Pages for the committed tokens and the next span."""
-        G.kv_pages_resize(self.dims, self.ctx + self.shape.n_tok, self.table, self.page_ref, self.page_ws, self.page_ws.numel(),
-                          self.status, stream)
+        with on_stream(stream):      # the lengths are summed where they are used
+            torch.add(self.ctx, self.shape.n_tok, out=self.want)
+        G.kv_pages_resize(self.dims, self.want, self.table, self.page_ref, self.page_ws, self.page_ws.numel(), self.status, stream)
 
     def attend(self, y: int, stream=None):
         """Attention layer y over the span: norm and rotary, then attention."""
