@@ -572,6 +572,14 @@ size_t attn_workspace_bytes(const attn_dims *dims, int32_t n_tok);
  *   temperature [B] f32 (>= 0) or NULL (all 1)
  *   uniforms    [B][N] f32 in [0, 1), entry 0 ignored
  *   noise       [B][V] f32 > 0
+ * The next token in the next step: it is a sample already and must not be tested
+ * again (a refusal would undo it, and what is committed would no longer be
+ * distributed as the target's samples). It has neither a recurrent state nor a
+ * cache row yet, so it is node 1 of the next span, whose row 0 is the accepted
+ * node's; the caller gives that node uniforms[b][1] = 0. With it node 1, the
+ * root's first child, is accepted at once (0 < p), the root's other children are
+ * not tried, and the drafts proper are the nodes below node 1. The same goes for
+ * the token that was sampled from a prompt's last row.
  * Outputs: accept_len [B], accept_node [B] as spec_accept_greedy;
  *   next_token [B] int32; token_prob [B][N] f32 (nullable): entry n >= 1 the
  *   target's p(tokens[n]) after its parent, entry 0 p(next_token) after the

@@ -13,6 +13,11 @@ synchronisation, what such a target does with a drafted span:
     spec_accept_sample     acceptance from given random numbers
     gdn_rollback_restore   GDN states of the accepted node
     kv_commit_path         cache rows of the accepted path, the new lengths
+    (carry)                the next token as node 1 of the next span
+
+Node 1 of every span is a token that has been sampled (by the step before, for
+the first step by the prompt's last row) but not processed yet: it is accepted
+without another test (uniform 0), and a step commits one token at least.
 
 The model around the calls (projections, feed-forward layers, the draft) is
 the caller's: inputs here are seeded random numbers of its shapes, as the
@@ -91,6 +96,7 @@ class HybridStep:
         self.noise = torch.empty((B, s.vocab), device=dev)
         self.accept_len, self.accept_node, self.next_token = (torch.zeros((B,), dtype=torch.int32, device=dev) for _ in range(3))
         self.token_prob = torch.zeros((B, s.n_nodes), device=dev)
+        self.every = torch.arange(B, device=dev)
         self.status = torch.zeros((1,), dtype=torch.int32, device=dev)
 
         def workspace(n):
@@ -104,6 +110,7 @@ class HybridStep:
     def draw(self):
         """New random numbers for the next acceptance."""
         self.uniforms.uniform_(generator=self.generator)
+        self.uniforms[:, 1] = 0.0       # node 1 is a sample already
         self.noise.exponential_(generator=self.generator).clamp_(min=1e-10)
 
     def make_room(self, stream=None):
@@ -140,13 +147,22 @@ class HybridStep:
         G.kv_commit_path(self.dims, s.n_nodes, g.parent, self.accept_node, self.ctx, self.table, self.k_pages, self.v_pages,
                          self.ctx_next, self.status, stream)
 
+    def carry(self, stream=None):
+        """The next span's node 1, the next token, and its row 0, the accepted
+        node's. The other nodes' tokens and rows are the caller's to make."""
+        with on_stream(stream):
+            self.gdn.tokens[:, 1] = self.next_token
+            self.gdn.logits[:, 0] = self.gdn.logits[self.every, self.accept_node.long()]
+
     def step(self):
-        """One step on the current stream; afterwards ctx holds the new lengths."""
+        """One step on the current stream; afterwards ctx holds the new lengths
+        and the next span begins with the sampled next token."""
         self.gdn.verify()
         for y in range(self.attn.layers):
             self.attend(y)
         self.accept()
         self.commit()
+        self.carry()
         self.ctx.copy_(self.ctx_next)
         self.make_room()
 

@@ -45,3 +45,30 @@ def test_room_is_made_on_the_stream_that_is_given(handle):
     want = [-(-(n + T) // 16) for n in (90, 3, 17)]
     assert [(row >= 0).sum().item() for row in table] == want
     assert int(ref.sum()) == sum(want) and int(h.status.item()) == 0
+
+
+def test_the_next_token_begins_the_next_span():
+    """Node 1 is the token sampled last, row 0 the row it was drawn from, and it
+    is not tested a second time."""
+    h = small(ctx=(40, 3, 0, 9), temperature=0.5)
+    for step in range(6):
+        h.draw()
+        tokens, length = h.gdn.tokens.clone(), h.ctx.clone()
+        rows = h.gdn.logits.clone()
+        h.step()
+        assert int(h.status.item()) == 0
+        node, taken = h.accept_node.tolist(), h.accept_len.tolist()
+        for b in range(4):
+            assert taken[b] >= 1, step
+            i = node[b]
+            while h.gdn.parent_host[b][i] > 0:
+                i = int(h.gdn.parent_host[b][i])
+            assert i == 1                                      # the root's first child is on the path
+            assert int(h.ctx[b]) == int(length[b]) + taken[b]
+            assert torch.equal(h.gdn.logits[b, 0], rows[b, node[b]])
+            assert torch.equal(h.gdn.logits[b, 1:], rows[b, 1:])
+        assert torch.equal(h.gdn.tokens[:, 1], h.next_token) and torch.equal(h.gdn.tokens[:, 2:], tokens[:, 2:])
+        # the next step's probability of node 1 is what the token was drawn with
+        drawn = h.token_prob[:, 0].clone()
+        h.accept()
+        torch.testing.assert_close(h.token_prob[:, 1], drawn, rtol=1e-5, atol=0)
