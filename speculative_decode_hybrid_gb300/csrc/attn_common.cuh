@@ -1,10 +1,10 @@
-// What the attention kernels share: their arguments, a node's root path as a
-// bit mask, and the join of partial results.
+// What the attention kernels share: their arguments and a node's root path as a
+// bit mask.
 #pragma once
 
 #include <cstdint>
 
-#include "gdn_device.cuh"
+#include "attn_device.cuh"
 
 namespace gdnattn {
 

@@ -23,7 +23,7 @@
 #include <initializer_list>
 #include <type_traits>
 
-#include "gdn_device.cuh"
+#include "attn_device.cuh"
 #include "gdn_host.h"
 #include "gdnspec.h"
 

@@ -45,8 +45,8 @@
 
 #include "attn_common.cuh"
 #include "attn_host.h"
+#include "attn_tc.cuh"
 #include "gdn_host.h"
-#include "gdn_tc.cuh"
 #include "gdnspec.h"
 
 namespace {

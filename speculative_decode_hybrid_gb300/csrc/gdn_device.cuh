@@ -38,10 +38,7 @@ __device__ __forceinline__ bool in_buf(const void *ptr, size_t n, Buf b, int32_t
 // writes are visible; returns at once for a grid launched without the
 // attribute. Every kernel of this library calls it before its first global
 // memory access. pdl_launch_dependents(): let the grid launched after this
-// one be scheduled now (it still waits for this grid's completion). The last
-// kernel of a call does so only after its own wait: a caller's next kernel may
-// rely on everything before the kernel it overlaps being complete
-// (GDN_VERIFY_STATE_READY).
+// one be scheduled now (it still waits for this grid's completion).
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
@@ -132,32 +129,6 @@ __device__ __forceinline__ float dot4(float4 a, float4 b, float acc) {
     acc = fmaf(a.z, b.z, acc);
     acc = fmaf(a.w, b.w, acc);
     return acc;
-}
-
-// Two f32 operations in one instruction.
-__device__ __forceinline__ float2 fma2(float2 x, float2 y, float2 z) {
-    float2 r;
-    asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
-        "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
-        : "=f"(r.x), "=f"(r.y)
-        : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y), "f"(z.x), "f"(z.y));
-    return r;
-}
-__device__ __forceinline__ float2 add2(float2 x, float2 y) {
-    float2 r;
-    asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
-        "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
-        : "=f"(r.x), "=f"(r.y)
-        : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y));
-    return r;
-}
-__device__ __forceinline__ float2 mul2(float2 x, float2 y) {
-    float2 r;
-    asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
-        "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
-        : "=f"(r.x), "=f"(r.y)
-        : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y));
-    return r;
 }
 
 // SiLU(y) = y / (1 + e^-y) with the fast exponential and division

@@ -1,7 +1,7 @@
 // tcgen05 (5th-generation tensor core) helpers for sm_100-family GPUs:
 // tensor memory allocation, shared-memory operand descriptors, kind::tf32
 // MMA with the accumulator in tensor memory, completion through an mbarrier,
-// and tensor-memory loads/stores; kind::f16 MMA with bf16 operands. Inline PTX only.
+// and tensor-memory loads/stores. Inline PTX only.
 //
 // Operand layout: K-major tiles in shared memory with the 128-byte swizzle.
 // A tile of `rows` rows keeps each row's K elements in 128-byte chunks: chunk
@@ -33,26 +33,6 @@ __device__ __forceinline__ uint64_t smem_desc_sw128(unsigned saddr) {
 // K-major, M x N.
 __host__ __device__ constexpr unsigned idesc_tf32(unsigned M, unsigned N) {
     return (1u << 4) | (2u << 7) | (2u << 10) | ((N >> 3) << 17) | ((M >> 4) << 24);
-}
-
-// Descriptor of an MN-major tile of 16-bit values (rows along K, 64 values of
-// M or N in a row's 128 bytes) with the 128-byte swizzle: `block` bytes from
-// one 64-value block of M or N to the next, 1024 bytes from 8 rows to the next
-// 8. One MMA step consumes K = 16 rows, 2048 bytes of each block.
-__device__ __forceinline__ uint64_t smem_desc_sw128_mn(unsigned saddr, unsigned block) {
-    uint64_t d = 0;
-    d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
-    d |= (uint64_t)(block >> 4) << 16;
-    d |= (uint64_t)(1024u >> 4) << 32;
-    d |= (uint64_t)1 << 46;
-    d |= (uint64_t)2 << 61;
-    return d;
-}
-
-// Instruction descriptor of kind::f16: f32 accumulator, bf16 A (K-major) and
-// bf16 B (K-major, or MN-major), M x N.
-__host__ __device__ constexpr unsigned idesc_bf16(unsigned M, unsigned N, bool b_mn_major) {
-    return (1u << 4) | (1u << 7) | (1u << 10) | ((b_mn_major ? 1u : 0u) << 16) | ((N >> 3) << 17) | ((M >> 4) << 24);
 }
 
 // x rounded to tf32 (nearest, ties away from zero), as an f32 whose low 13
@@ -105,25 +85,6 @@ __device__ __forceinline__ void mma_tf32_ts(unsigned d_tmem, unsigned a_tmem, ui
         : "memory");
 }
 
-// The same two with bf16 operands (kind::f16, K = 16 a step); a tensor-memory A
-// holds two values in a 32-bit column.
-__device__ __forceinline__ void mma_bf16_ss(unsigned d_tmem, uint64_t a_desc, uint64_t b_desc, unsigned idesc,
-                                            bool accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate ? 1u : 0u)
-        : "memory");
-}
-__device__ __forceinline__ void mma_bf16_ts(unsigned d_tmem, unsigned a_tmem, uint64_t b_desc, unsigned idesc,
-                                            bool accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate ? 1u : 0u)
-        : "memory");
-}
-
 // The mbarrier at `bar` gets one arrival when every MMA this thread issued
 // has completed.
 __device__ __forceinline__ void mma_commit(unsigned bar) {
@@ -152,17 +113,6 @@ __device__ __forceinline__ void tmem_st8(unsigned taddr, const unsigned (&v)[8])
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
                  "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
                  : "memory");
-}
-// Warp-collective: 32 consecutive 32-bit columns of this thread's lane.
-__device__ __forceinline__ void tmem_st32(unsigned taddr, const unsigned (&v)[32]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
-        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
-        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]),
-        "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
-        "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
-        : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
