@@ -556,12 +556,13 @@ Cut cut_of(const attn_dims *dims, int n_tok) {
     const int d = dims->d_head, rows = n_tok * (dims->h_q / dims->h_kv);
     const int64_t slots = (int64_t)dims->table_width * dims->page_tokens;  // the longest request that the table holds
     Cut c{};
-    int tile, held = 152, slot_warps = 1;  // slots that a block takes at a time, blocks that the GPU holds
+    const int sms = gdnhost::sm_count();
+    int tile, held = sms > 0 ? sms : 152, slot_warps = 1;  // slots that a block takes at a time, blocks that the GPU holds
     if (rows <= (d == 256 ? 32 : 8)) {
         const int block = few_rows(rows);
         c.row_blocks = (rows + block - 1) / block;
         tile = 128;
-        if (block < 8 && d < 256) held = 304;
+        if (block < 8 && d < 256) held *= 2;
     } else {
         c.lane_rows = d == 256 || rows <= 32 ? 4 : 8;
         // the fewest rows of padding, then the fewest copies of a tile

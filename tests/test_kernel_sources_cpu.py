@@ -31,3 +31,11 @@ def test_attention_takes_tensor_memory_after_the_grid_wait():
     before would hang with one that allocates after letting it start."""
     text = code(os.path.join(B.CSRC, "attn_tc.cu"))
     assert text.count("tmem_alloc") == 1 and 0 < text.index("pdl_wait()") < text.index("tmem_alloc")
+
+
+def test_the_number_of_sms_is_asked_for():
+    """152 stands only where the device does not answer."""
+    for path in SOURCES:
+        for line in code(path).splitlines():
+            if re.search(r"\b(152|304)\b", line):
+                assert re.search(r"sms (> 0 \?|<= 0 \? 152)", line), (os.path.basename(path), line.strip())
