@@ -35,7 +35,9 @@ constexpr int kMaxParts = 128;
 // alone 21); 8 requests', 16 heads of 128 over 2,000 15.3 us with the join (20.6;
 // 4.1); one over 777 10.8 us (14.7), two launches. Bound by the wait for the loads,
 // 64 KB of them in flight on an SM, and by about as many operations for the sums
-// over lanes as for the products.
+// over lanes as for the products. Two blocks an SM leave 128 registers a thread:
+// with four rows some 212 bytes of a thread spill (128 and 64 wide), with one or
+// two, and in the one-block forms, none.
 template <int D, int R>
 struct Few {
     static constexpr int kLanes = D == 64 ? 16 : 32, kGroups = 32 / kLanes, kC = D / (4 * kLanes);

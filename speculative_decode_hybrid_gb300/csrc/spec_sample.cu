@@ -25,7 +25,9 @@
 // depend on the sums is read while they are still being taken. The first launch
 // is bound by the logits' bytes (38 us for 224 MB, 0.87 of the measured copy rate),
 // the second by latency: 14 us for the same 16 requests, in which a row's loads
-// follow the walk, the walk the statistics, and those the tokens. Its blocks are
+// follow the walk, the walk the statistics, and those the tokens. A rejected sibling
+// of a sampled draft is one more pass over its row and the draft's by the request's
+// cluster: 60 us for those 16 trees with draft rows, 52 with fixed candidates. Its blocks are
 // held to 64 registers: at one block an SM, only 15 of the 16 clusters of eight
 // fit the GPU at once (47 us).
 #include <cooperative_groups.h>
