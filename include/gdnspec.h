@@ -89,10 +89,10 @@ typedef void *gdn_stream_t;
 #define GDN_DEV_TREE 0x8          /* a device parent array broke parent[i] in [0, i): the kernel
                                      used parent i-1 for that node (verify) or left it unmatched
                                      (acceptance) instead of reading out of bounds */
-#define GDN_DEV_SCHED 0x10        /* verify: a CTA gave up waiting for an asynchronous hardware
-                                     operation (the answer to a work-stealing request, a
-                                     tensor-core product, or (the _pipelined calls) an input
-                                     flag); its outputs are incomplete */
+#define GDN_DEV_SCHED 0x10        /* verify, attention: a CTA gave up waiting for an asynchronous
+                                     hardware operation (the answer to a work-stealing request,
+                                     a copy, a tensor-core product, or (the _pipelined calls) an
+                                     input flag); its outputs are incomplete */
 #define GDN_DEV_BOUNDS 0x20       /* debug builds of the library only (GDN_DEBUG_BOUNDS): a kernel
                                      skipped a global access that fell outside its buffer */
 #define GDN_DEV_LENGTH 0x40       /* a context length, or a count of tokens asked for, that its row of

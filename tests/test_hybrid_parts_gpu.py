@@ -72,3 +72,12 @@ def test_the_next_token_begins_the_next_span():
         drawn = h.token_prob[:, 0].clone()
         h.accept()
         torch.testing.assert_close(h.token_prob[:, 1], drawn, rtol=1e-5, atol=0)
+
+
+def test_room_on_the_current_and_the_default_stream():
+    h = small()
+    for stream in (None, 0, torch.cuda.default_stream()):
+        h.ctx.add_(16)
+        h.make_room(stream)
+        assert [(row >= 0).sum().item() for row in h.table.cpu()] == [-(-(n + h.shape.n_tok) // 16) for n in h.ctx.tolist()]
+    assert int(h.status.item()) == 0
