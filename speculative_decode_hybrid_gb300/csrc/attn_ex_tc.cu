@@ -5,7 +5,8 @@
 //
 // Scores. x = q k becomes, in powers of two, y = c - 2 c / (1 + 2^(x cap_in)) with
 // a cap (c tanh(scale x / cap), by one exponential and one reciprocal, off by
-// some 2^-20 c), scale x without; a bias by distance adds slope (slot - r), with
+// some 2^-20 c; caps above 128: cap_far), scale x without; a bias by distance adds
+// slope (slot - r), with
 // r the node's position, or 0 for a slope below 0: a row's constant does not
 // matter, and so the bias is small where the weight lies. A segment's tiles are taken
 // from the last to the first, so that such a bias does not raise the maximum tile by
@@ -254,12 +255,57 @@ __device__ __forceinline__ float min_nan(float x, float y) {
     return r;
 }
 
+// What changes the scores: nothing; a cap up to kMostOfNear or a bias; a cap above it (and
+// a bias).
+enum Scores { kPlain, kNear, kFar };
+
+// The form of one exponential, c - 2 c / (1 + e), is a difference of two numbers as large as
+// the cap, off by 2^-20 of it whatever the score: at 128 (in powers of two here) a sixteenth
+// of the half step of a bf16 weight. For larger caps a score below a quarter of the cap is
+// z (1 - u^2 / 3 + 2 u^4 / 15 - ...), u = z / c, its next term 10^-8; one that is not loses
+// 2^-18 of itself. A kernel of its own for them: as a branch it cost the others registers
+// (248 bytes of spills; 16 spans of 16 over up to 8,000 slots with a cap of 50 107 us
+// instead of 89). Those spans with a cap of 200 take 104 us, 89 by the near form.
+constexpr float kMostOfNear = 128.f * gdnattn::kLog2e;
+
+template <int K>
+__device__ __forceinline__ void cap_far(const ExArgs &ex, unsigned (&x)[K][32], float scale_log2) {
+    const float half = ex.cap_in * 0.34657359f;  // ln 2 / 2
+    float top = 0.f;
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) top = max3(top, fabsf(__uint_as_float(x[k][i])), fabsf(__uint_as_float(x[k][i + 1])));
+    auto series = [&](float s) {
+        const float u = s * half, u2 = u * u;
+        return s * scale_log2 * fmaf(u2, fmaf(u2, fmaf(u2, fmaf(u2, 62.f / 2835, -17.f / 315), 2.f / 15), -1.f / 3), 1.f);
+    };
+    if (__all_sync(~0u, top * half <= 0.25f)) {  // (a NaN is one in either form)
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+            for (int i = 0; i < 32; ++i) x[k][i] = __float_as_uint(series(__uint_as_float(x[k][i])));
+    } else {
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+                const float s = __uint_as_float(x[k][i]);
+                float r;
+                asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + ex2(min_nan(s * ex.cap_in, 30.f))));
+                x[k][i] = __float_as_uint(fabsf(s) * half <= 0.25f ? series(s) : fmaf(r, -2.f * ex.cap, ex.cap));
+            }
+    }
+}
+
 // Scores as they are changed: the cap, then the bias. at: the first one's slot less the
 // row's reference. Four scores share a reciprocal: no NaN that is not seen may be among
 // them.
-template <int K>
+template <Scores kScores, int K>
 __device__ __forceinline__ void change(const ExArgs &ex, unsigned (&x)[K][32], int at, float slope, float scale_log2) {
-    if (ex.cap > 0.f) {
+    if (kScores == kFar) {
+        cap_far(ex, x, scale_log2);
+    } else if (ex.cap > 0.f) {
         const float c2 = -2.f * ex.cap;
 #pragma unroll
         for (int k = 0; k < K; ++k)
@@ -354,15 +400,16 @@ __device__ __noinline__ void restore(const Table &t, float4 *part, int step, __n
     }
 }
 
-// kChanged: with a cap or a bias. A kernel of its own: the code of both is longer than
+// With a cap or a bias a kernel of its own: the code of both is longer than
 // all the rest of a tile's.
-template <int D, int P, bool kChanged>
+template <int D, int P, Scores kScores>
 __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
 attend_ex(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
           const __grid_constant__ AttnArgs a, const __grid_constant__ ExArgs ex, const __grid_constant__ Plan plan,
           const __grid_constant__ Pieces pieces) {
     using S = Shape<D>;
     constexpr int kN = S::kN, kStages = S::kStages;
+    constexpr bool kChanged = kScores != kPlain;
     extern __shared__ char raw[];
     __shared__ Control<D> c;
     char *base = raw + ((1024 - (saddr(raw) & 1023)) & 1023);
@@ -690,7 +737,7 @@ attend_ex(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUt
                     };
                     if (kChanged) {
                         if (edge && ex.cap > 0.f) hide(0u);
-                        change(ex, x, my_first - ref, slope, a.scale_log2);
+                        change<kScores>(ex, x, my_first - ref, slope, a.scale_log2);
                         if (edge && ex.slopes && a.parent && !s.shared)
 #pragma unroll
                             for (int k = 0; k < kSlices; ++k) place_nodes(x[k], my_first + k * 32 - ctx, slope, path);
@@ -1078,15 +1125,15 @@ struct Sizes {
 template <int D, int P>
 int launch(const attn_dims *d, const AttnArgs &a, const ExArgs &x, void *ws, cudaStream_t st) {
     using S = Shape<D>;
-    static bool set[2][256] = {};
-    const bool changed = x.cap > 0.f || x.slopes;
-    const auto kernel = changed ? attend_ex<D, P, true> : attend_ex<D, P, false>;
+    static bool set[3][256] = {};
+    const Scores scores = x.cap > kMostOfNear ? kFar : x.cap > 0.f || x.slopes ? kNear : kPlain;
+    const auto kernel = scores == kFar ? attend_ex<D, P, kFar> : scores == kNear ? attend_ex<D, P, kNear> : attend_ex<D, P, kPlain>;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 256) return GDN_ERR_CUDA;
-    if (!set[changed][dev]) {
+    if (!set[scores][dev]) {
         if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kSmem) != cudaSuccess)
             return GDN_ERR_CUDA;
-        set[changed][dev] = true;
+        set[scores][dev] = true;
     }
     CUtensorMap k_map, v_map;
     if (!pool_map(&k_map, d, a.k_pages, S::kN) || !pool_map(&v_map, d, a.v_pages, S::kN)) return GDN_ERR_CUDA;
