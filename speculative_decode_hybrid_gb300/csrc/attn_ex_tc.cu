@@ -6,14 +6,14 @@
 // Scores. x = q k becomes, in powers of two, y = c - 2 c / (1 + 2^(x cap_in)) with
 // a cap (c tanh(scale x / cap), by one exponential and one reciprocal, off by
 // some 2^-20 c; caps above 128: cap_far), scale x without; a bias by distance adds
-// slope (slot - r), with
-// r the node's position, or 0 for a slope below 0: a row's constant does not
-// matter, and so the bias is small where the weight lies. A segment's tiles are taken
-// from the last to the first, so that such a bias does not raise the maximum tile by
-// tile. Slots before a window or
-// a document are whole tiles left out, and masked in the tiles where they end; V
-// is zeroed where no row sees it, and what is no number there is kept for the
-// rows that do, as attn_tc.cu does for the drafted nodes.
+// slope (slot - r), with r the node's position, or for a slope below 0 the first slot
+// that the row sees: a row's constant does not matter, and so the bias is small where
+// the weight lies (from slot 0 it would have lost whole units 8 million slots in). A
+// segment's tiles are taken from the last to the first, so that a bias for the near does
+// not raise the maximum tile by tile. Slots before a window or a document are whole
+// tiles left out, and masked in the tiles where they end; V is zeroed where no row sees
+// it, and what is no number there is kept for the rows that do, as attn_tc.cu does for
+// the drafted nodes.
 //
 // Shared prefixes. The list of work has an entry for every group of requests that
 // shares its first slots, with the rows of all its members against those slots,
@@ -704,7 +704,7 @@ attend_ex(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUt
                 if (ex.window && !s.shared) low = max(ex.first ? ex.first[s.b] : 0, min(ctx, ctx + path.depth - ex.window));
                 if (kChanged && ex.slopes) {
                     slope = ex.slopes[kv * plan.group + me.row - (t - 1) * plan.group] * gdnattn::kLog2e;
-                    ref = slope >= 0.f ? (s.shared ? a.ctx[me.b] : ctx) + path.depth - 1 : 0;
+                    ref = slope >= 0.f ? (s.shared ? a.ctx[me.b] : ctx) + path.depth - 1 : ex.plan ? 0 : low;
                 }
             }
             constexpr int kCols = kN / 2, kSlices = kCols / 32;  // of a tile, this thread's

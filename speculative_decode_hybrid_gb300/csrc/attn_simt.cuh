@@ -85,8 +85,9 @@ __device__ __forceinline__ RowAt row_of(const AttnArgs &a, const X &x, const Vie
 
 // What a row sees of the committed slots (from `low` on), and its bias: slope (in
 // powers of two) times a slot's position less `ref`. A row's constant does not matter:
-// ref is the node's own position, or 0 for a slope below 0, so that the bias is
-// small where the weight lies.
+// ref is the node's own position, or for a slope below 0 the first slot that the row sees
+// (with a plan, whose passes see parts of the row, that is 0), so that the bias is small
+// where the weight lies.
 struct RowInfo {
     int low, position, ref;
     float slope;
@@ -101,7 +102,7 @@ __device__ __forceinline__ RowInfo info_of(const AttnArgs &a, const Changed &x, 
     if (x.x.slopes) {
         r.slope = x.x.slopes[kv * group + at.row % group] * kLog2e;
         r.position = (x.shared ? a.ctx[at.b] : v.ctx) + depth - 1;
-        r.ref = r.slope >= 0.f ? r.position : 0;
+        r.ref = r.slope >= 0.f ? r.position : x.x.plan ? 0 : r.low;
     }
     return r;
 }
