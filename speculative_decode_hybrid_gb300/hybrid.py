@@ -165,9 +165,9 @@ class HybridStep:
     def fork(self, src, dst, stream=None):
         """Requests dst become copies of src: cache pages shared (tails copied), GDN
         states, the span so far; room for their next spans."""
-        src, dst = (torch.as_tensor(list(x), dtype=torch.int32).to(self.every.device) for x in (src, dst))
-        g, n = self.gdn, len(dst)
-        with on_stream(stream):
+        with on_stream(stream):      # the request numbers are made where they are read
+            src, dst = (torch.as_tensor(list(x), dtype=torch.int32).to(self.every.device) for x in (src, dst))
+            g, n = self.gdn, len(dst)
             self.want.fill_(-1)
             self.want[dst.long()] = 0
         G.kv_pages_resize(self.dims, self.want, self.table, self.page_ref, self.page_ws, self.page_ws.numel(), self.status, stream)
