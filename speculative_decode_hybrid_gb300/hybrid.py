@@ -164,9 +164,15 @@ class HybridStep:
 
     def fork(self, src, dst, stream=None):
         """Requests dst become copies of src: cache pages shared (tails copied), GDN
-        states, the span so far; room for their next spans."""
+        states, the span so far; room for their next spans. The dst differ from each
+        other and from every src."""
+        src, dst = ([int(b) for b in x] for x in (src, dst))
+        if len(src) != len(dst) or len(set(dst)) != len(dst) or set(src) & set(dst):
+            raise ValueError("a fork needs a source for each of its destinations, which differ from each other and from every source")
+        if not all(0 <= b < self.shape.batch for b in src + dst):
+            raise ValueError("a fork's requests lie in [0, %d)" % self.shape.batch)
         with on_stream(stream):      # the request numbers are made where they are read
-            src, dst = (torch.as_tensor(list(x), dtype=torch.int32).to(self.every.device) for x in (src, dst))
+            src, dst = (torch.as_tensor(x, dtype=torch.int32).to(self.every.device) for x in (src, dst))
             g, n = self.gdn, len(dst)
             self.want.fill_(-1)
             self.want[dst.long()] = 0

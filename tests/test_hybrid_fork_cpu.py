@@ -77,3 +77,14 @@ def test_all_that_a_fork_makes_is_on_its_stream(monkeypatch):
     assert w.outside == [] and set(w.streams) == {77}
     assert [n for n, _ in notes.calls] == ["kv_pages_resize", "kv_pages_fork", "kv_pages_resize"]
     assert all(a[-1] == 77 for _, a in notes.calls)
+
+
+@pytest.mark.parametrize("src,dst", [([0], [0]), ([0, 1], [1, 2]), ([0, 2], [1, 1]), ([0], [4]), ([4], [0]), ([-1], [1]), ([0], [-1]),
+                                     ([0], [1, 2]), ([0, 0], [1])], ids=str)
+def test_requests_that_cannot_be_forked(monkeypatch, src, dst):
+    """A copy of itself or of one that is being replaced, the same place twice, numbers that are none of the batch, lists
+    of different lengths: refused before anything is queued or given back."""
+    h, notes = step(monkeypatch)
+    with Where(monkeypatch) as w, pytest.raises(ValueError):
+        h.fork(src, dst)
+    assert notes.calls == [] and w.streams == []
