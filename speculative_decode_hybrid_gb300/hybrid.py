@@ -164,24 +164,28 @@ class HybridStep:
 
     def fork(self, src, dst, stream=None):
         """Requests dst become copies of src: cache pages shared (tails copied), GDN
-        states, the span so far; room for their next spans. The dst differ from each
-        other and from every src."""
+        states, the span so far (its tree and tokens, node 1 with them, and the target's
+        rows); room for their next spans. The caller's inputs and the requests' limits
+        stay. The dst differ from each other and from every src."""
         src, dst = ([int(b) for b in x] for x in (src, dst))
         if len(src) != len(dst) or len(set(dst)) != len(dst) or set(src) & set(dst):
             raise ValueError("a fork needs a source for each of its destinations, which differ from each other and from every source")
         if not all(0 <= b < self.shape.batch for b in src + dst):
             raise ValueError("a fork's requests lie in [0, %d)" % self.shape.batch)
+        g = self.gdn
+        if g.tree:      # (the workload's own array stays)
+            g.parent_host = g.parent_host.copy()
+            g.parent_host[dst] = g.parent_host[src]
         with on_stream(stream):      # the request numbers are made where they are read
-            src, dst = (torch.as_tensor(x, dtype=torch.int32).to(self.every.device) for x in (src, dst))
-            g, n = self.gdn, len(dst)
+            of, to = (torch.as_tensor(x, dtype=torch.int32).to(self.every.device) for x in (src, dst))
             self.want.fill_(-1)
-            self.want[dst.long()] = 0
+            self.want[to.long()] = 0
         G.kv_pages_resize(self.dims, self.want, self.table, self.page_ref, self.page_ws, self.page_ws.numel(), self.status, stream)
-        G.kv_pages_fork(self.dims, n, src, dst, self.table, self.ctx, self.page_ref, self.k_pages, self.v_pages, self.page_ws,
+        G.kv_pages_fork(self.dims, len(dst), of, to, self.table, self.ctx, self.page_ref, self.k_pages, self.v_pages, self.page_ws,
                         self.page_ws.numel(), self.status, stream)
         with on_stream(stream):
-            for x in (g.ssm_state, g.conv_state, g.tokens, g.logits):
-                x[dst.long()] = x[src.long()]
+            for x in (g.ssm_state, g.conv_state, g.tokens, g.logits) + ((g.parent,) if g.tree else ()):
+                x[to.long()] = x[of.long()]
         self.make_room(stream)
 
     def plan(self, stream=None):

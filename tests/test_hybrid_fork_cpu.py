@@ -88,3 +88,17 @@ def test_requests_that_cannot_be_forked(monkeypatch, src, dst):
     with Where(monkeypatch) as w, pytest.raises(ValueError):
         h.fork(src, dst)
     assert notes.calls == [] and w.streams == []
+
+
+def test_the_tree_goes_with_its_tokens(monkeypatch):
+    """A tree of each request: the copy has its source's, in the host's array too; the array that was given is left as it was."""
+    h, _ = step(monkeypatch, tree=True)
+    g = h.gdn
+    g.parent_host[0] = [-1, 0, 0, 1, 1]
+    given, before = g.parent_host, g.parent_host.copy()
+    copied = []
+    monkeypatch.setattr(torch.Tensor, "__setitem__", lambda self, i, v: copied.append(self))
+    h.fork([0, 0], [1, 3])
+    np.testing.assert_array_equal(g.parent_host, before[[0, 0, 2, 0]])
+    np.testing.assert_array_equal(given, before)
+    assert any(t is g.parent for t in copied) and any(t is g.tokens for t in copied)

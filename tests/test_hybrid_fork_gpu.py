@@ -48,3 +48,20 @@ def test_forks_on_the_stream_that_is_given(handle):
     assert int(h.status.item()) == 0
     for x, y in zip(held(want), held(h)):
         assert torch.equal(x, y)
+
+
+def test_forked_trees():
+    """Each request has a tree of its own: a copy's acceptance with its source's random numbers is its source's."""
+    h = small(wid=3)
+    assert not (h.gdn.parent[0] == h.gdn.parent[2]).all()
+    h.fork([0, 0], [2, 3])
+    for _ in range(2):
+        h.draw()
+        for x in (h.uniforms, h.noise):
+            x[2:] = x[0]
+        h.step()
+        torch.cuda.synchronize()
+        assert int(h.status.item()) == 0
+        for x in (h.gdn.parent, h.accept_len, h.accept_node, h.next_token, h.ctx, h.gdn.tokens, h.token_prob):
+            assert torch.equal(x[2], x[0]) and torch.equal(x[3], x[0])
+        assert (h.gdn.parent.cpu().numpy() == h.gdn.parent_host).all()
