@@ -560,8 +560,10 @@ size_t attn_workspace_bytes(const attn_dims *dims, int32_t n_tok);
  *   p_t - p_s < window                       window > 0 (its own slot is always seen)
  *   s >= first[b]                            first given: the request's document
  *                                            begins at slot first[b] of its row
- * Slots that no node sees are not read, nor are their pages' table entries: they
- * may be freed. first[b] outside [0, ctx_len[b]] leaves the request out
+ * Slots that no node sees are not read, nor are their pages' table entries: a
+ * caller that keeps its own tables may have given those pages away (kv_pages_resize
+ * does not do it: it takes back the end of a row, and takes a new page for an entry
+ * that is missing in front). first[b] outside [0, ctx_len[b]] leaves the request out
  * (GDN_DEV_LENGTH). Where an NaN or infinity lies in a slot that a node does not
  * see, the node's result does not change.
  *
@@ -612,8 +614,13 @@ size_t attn_ex_workspace_bytes(const attn_dims *dims, int32_t n_tok);
  * attn_tree_verify_ex with such a plan, of the same dims, table and lengths. The
  * results are theirs up to the order of sums. mods may change scores (softcap,
  * slopes); window and first must be none (GDN_ERR_DIMS).
- * They read less and launch more: where a prefix is short or (f32) its keys and
- * values stay in L2, theirs are faster.
+ * They read less and launch more, and what they save is read from L2 while it
+ * fits there. Plan included, against attn_verify_span_ex, in us: bf16, 8 single
+ * tokens, 16 heads on 2, 128 wide: 21 and 16 over 2,000 shared slots, 25 and 24 over
+ * 10,000, 27 and 32 over 20,000; 256 wide over 32,000, a layer of four 35 and 66; 2 x
+ * 8 trees of 22 over 16,000, a layer of two 120 and 134 (attn_tree_verify 115). f32: no
+ * gain below some 50,000 slots, and its time grows with the square of the batch (512
+ * tokens of 256 prompts over 2,000 slots 1,693 and 330).
  *   workspace  at least attn_shared_workspace_bytes(dims, n_tok)
  * Limits: theirs, batch at most GDN_MAX_PREFIX_BATCH, and for bf16 their tile
  * limit with batch * n_tok in the place of n_tok. Returns as they do
@@ -697,12 +704,15 @@ size_t spec_accept_sample_workspace_bytes(int32_t batch, int32_t n_nodes);
  *   j < top_k,   w_j >= min_p,   and  sum_{i<j} w_i < top_p * (the sum of the first top_k w);
  * the first one always. p = w / (sum of the kept w), 0 for the others; the token
  * is the largest p(v) / noise[v] (lowest index on ties), a sample of p when the
- * noise is exponential with mean 1. Sums and borders in 44-bit integers: the
- * same from call to call.
+ * noise is exponential with mean 1. The sums that place a border, and weights next
+ * to min_p, are integers in units of 2^-44, so that a border is off by at most
+ * 2^-28 + V 2^-42 of the first top_k's sum (or 2^-44 in a weight); the sum that p is divided by is f32, its
+ * terms added in a fixed order (off by less than 5e-6 at V = 151,936). Results are
+ * the same from call to call.
  * Temperature 0 (or below, or NaN) is the limit: w = 1 for the largest logits, 0
- * for the others. A NaN or +inf among a row's logits, or a row with none above
- * -inf: token 0, its probability and its row of probs NaN, its logits kept as
- * they are, GDN_DEV_NAN_LOGIT.
+ * for the others (logits less than 5e-37 below the largest count as it). A NaN or
+ * +inf among a row's logits, or a row with none above -inf: token 0, its probability
+ * and its row of probs NaN, its logits kept as they are, GDN_DEV_NAN_LOGIT.
  *
  *   logits      [rows][V] f32
  *   temperature, top_p, min_p [ceil(rows / rows_per_request)] f32, top_k the

@@ -8,7 +8,11 @@
 // Shared, plan included, against each request for itself (8 heads on 2, 128 wide, 8
 // requests' tokens): 64 and 60 us over 20,000 slots, whose 41 MB stay in L2, 115 and 144
 // over 50,000, 325 and 541 over 200,000; 8 x 16 rows over 100,000 1,571 and 1,582, by
-// the f32 pipe's work, which is the same; 4 x 5 over 3,000 58 and 31, by launches.
+// the f32 pipe's work, which is the same; 4 x 5 over 3,000 58 and 31, by launches. The pass
+// over the groups has blocks for half as many groups as requests, each of all requests'
+// rows, most of which end at once: its grid grows with the square of the batch (single
+// tokens over 2,000 slots: 64 of 8 prompts 122 and 48, 512 of 64 609 and 282, 512 of 256
+// 1,693 and 330).
 #include "attn_ex_host.h"
 #include "attn_simt.cuh"
 

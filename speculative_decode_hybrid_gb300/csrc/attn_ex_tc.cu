@@ -24,6 +24,10 @@
 // blocks to the blocks' pieces, and join_rows adds them up on the scale of their
 // largest maximum.
 //
+// Weights are rounded to bf16 once for the second product, not in the divisor, as in
+// attn_tc.cu, where the form in two parts and its price stand: a result is 1.8e-3 to 2.3e-3
+// of its norm from the 64-bit one, of which the rounding of the result itself is 1.7e-3.
+//
 // Two threads a row, each with half of a tile's columns: 8 softmax warps hide more of
 // each other's waits than 4, and leave registers for what changes the scores. Where the
 // time goes, in cycles of a 128 x 128 x 128 tile: wait for the scores 240, their loads
@@ -40,9 +44,13 @@
 // slots 80 us with a bias and 89 with a cap (73 by the plain kernel), by the softmax
 // warps' work: a cap is another exponential and a quarter of a reciprocal a score.
 // Shared: 8 samples' tokens over 32,000 shared slots, 256 wide, 34 us a layer (66 each
-// for itself; the bytes 10), 2 x 8 trees of 22 nodes over 16,000 and 12,000
-// slots 119 to 123 us (134 each for itself; the products 43): tensor pipes 35 % busy, by the waits
-// between a tile's scores, weights and sums, and 128 short segments of some 11 us each.
+// for itself; the bytes 10), 2 x 8 trees of 22 nodes over 16,000 and 12,000 slots 119 to
+// 123 us (each for itself 134 by this kernel and 115 by the plain one; the products 43):
+// tensor pipes 35 % busy, by the waits between a tile's scores, weights and sums, and 128
+// short segments of some 11 us each. Prefixes that fit in L2 are read from there by the
+// calls that do not share: 8 single tokens, 128 wide, break even at some 10,000 slots.
+// Spills: none with changed scores; 30 to 34 bytes without at 64 and 128 wide, 100 in
+// join_rows (64 registers, four blocks an SM).
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -527,7 +535,7 @@ attend_ex(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUt
             bool ok = true;
             while (work.left > 0 && ok) {
                 Segment s;
-            next_segment<kN, P>(c.table, work, s);
+                next_segment<kN, P>(c.table, work, s);
                 if (s.n == 0) break;
                 ok = wait(saddr(&c.q_full), seg & 1, quit);
                 ++seg;
@@ -561,7 +569,7 @@ attend_ex(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUt
             bool ok = true;
             while (work.left > 0 && ok) {
                 Segment s;
-            next_segment<kN, P>(c.table, work, s);
+                next_segment<kN, P>(c.table, work, s);
                 if (s.n == 0) break;
                 for (int j = 0; j < s.n && ok; ++j, ++g) {
                     const int stage = g % kStages;

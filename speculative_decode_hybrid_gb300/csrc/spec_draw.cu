@@ -20,8 +20,8 @@
 // limits.
 //
 // The masses that top_p compares are integers, so that sums do not depend on the
-// order of the atomic additions, and accurate to some 2^-29, so that a token is on
-// the side of the border that it is on in exact arithmetic (f32 weights, off by
+// order of the atomic additions, and off by at most 2^-28 + V 2^-42 of the row's, so that a
+// token that is not that near the border is on the side that it is on in exact arithmetic (f32 weights, off by
 // up to 2^-20, would misplace one in a hundred borders among weights of 1e-4). An
 // element of the bin 2^(-n / 48) weighs 2^(-n / 48) (1 + z) with |z| < 2^-7: the
 // bin's mass is the sum of 1 + z in 28 fraction bits, in two halves that 32 bits hold
@@ -30,11 +30,13 @@
 // that state with these).
 //
 // Bound by latency: a row's phases follow one another, each with waits for the cluster
-// or for memory, and two blocks fit an SM. In cycles of one row of 151,936 with top-p:
-// load 2,400, maximum 2,400, histogram 7,100, search 7,000, gathering and picking 11,200,
-// noise 7,400, the token 3,200. That row takes 19 us, 16 rows with all limits 22; 272 rows
-// with top-p and their distributions 271, of which the bytes would take 49; without the
-// distributions 241, with a min-p alone, which needs neither histogram nor search, 122.
+// or for memory, and two blocks fit an SM. In cycles of one row of 151,936 with top-p
+// (clock64 in its first block, inputs in L2): load 2,600, maximum 2,500, histogram 7,300,
+// search 6,500, gathering and picking 9,500, noise 6,000, the token 3,000: 37,400 in all,
+// of the 19 us that the call takes; from memory 54,000. 16 rows with all limits take 22 us;
+// 272 rows with top-p and their distributions 271, of which the bytes would take 49; without
+// the distributions 241, with a min-p alone, which needs neither histogram nor search, 122.
+// At 64 registers a thread spills 144 bytes.
 // Measured and dropped: functions that are not inlined, for shorter code (408 us instead
 // of 350), the slice of the row 20, 36 or 60 clusters on asked for into L2 (338, 371 and
 // 300 us in a state that took 305 without), five to ten loads in flight instead of four

@@ -24,7 +24,9 @@ by distance use attn_*_ex.
 
 Node 1 of every span is a token that has been sampled (by the step before, for
 the first step by the prompt's last row) but not processed yet: it is accepted
-without another test (uniform 0), and a step commits one token at least.
+without another test (uniform 0), and a step commits one token at least. The first
+span's is whatever the workload begins with: a step that cuts it (limits, temperature
+0) refuses it and goes on from the root.
 
 The model around the calls (projections, feed-forward layers, the draft) is
 the caller's: inputs here are seeded random numbers of its shapes, as the
@@ -71,7 +73,9 @@ class HybridStep:
         filled with random keys and values). top_k, top_p, min_p: limits of the
         target's and the draft's distributions (0, 1, 0: none). drafts: the span's
         tokens past node 1 are drawn from a draft's logits (chains). share:
-        requests that share pages in front read them once; not with a window."""
+        requests that share pages in front read them once; not with a window. It
+        pays for prefixes of tens of thousands of slots (attn_verify_span_shared's
+        figures); below, the attention without it is as fast or faster."""
         if drafts and wl.parent is not None:
             raise ValueError("drafts are drawn for chains only")
         if share and attn.window:
